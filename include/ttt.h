@@ -62,6 +62,8 @@
 extern "C" {
 #endif
 
+/* Counts the changes to existing functions and types; functions are added
+ * under the same number. */
 #define TTT_ABI_VERSION 11
 
 typedef enum {
@@ -474,6 +476,184 @@ ttt_status ttt_input_projection(const ttt_params* p, int32_t d_model,
                                 const float* b_eta, float eta_base,
                                 void* q, void* k, void* v, float* eta,
                                 void* hip_stream);
+
+/*
+ * ---- around and beside the TTT scans ---------------------------------------
+ *
+ * The RMS norm in front of the input projection, the input projection from
+ * 8-bit operands, the short causal convolution over q, k or v, and a
+ * selective state space scan with the layouts of the TTT scans.  The
+ * conventions at the top of this file hold; in addition:
+ *  - Pointers to [..., width], [..., d] and [..., N] arrays and to states are
+ *    16-byte aligned, workspaces 256-byte aligned (else TTT_ERR_ARG).  Only
+ *    a workspace is ever scratch: two calls that may run at once need two.
+ *  - Of ttt_params these functions read B, H, T, d and io_dtype alone.
+ *  - Outputs overlap no input and no other output unless stated
+ *    (TTT_ERR_ALIAS).  Results are the same bit for bit from run to run.
+ *  - "8 bits" are e4m3 values (4 exponent and 3 mantissa bits, no infinity,
+ *    largest 448), one byte each.
+ */
+
+/*
+ * RMS norm with the residual's addition, row by row in fp32:
+ *   r = x + residual                     (r = x without a residual)
+ *   y = r / sqrt(mean(r^2) + eps) * weight
+ *   rows     >= 1; width a multiple of 8, at most 16384 (else
+ *            TTT_ERR_UNSUPPORTED); eps >= 0 (else TTT_ERR_ARG).
+ *   x        [rows,width] io_dtype.     weight [width] fp32.
+ *   residual [rows,width] io_dtype or NULL.
+ *   y        [rows,width] io_dtype, rounded once from fp32.
+ *   res_out  [rows,width] io_dtype: r rounded once (y is made from r before
+ *            that rounding).  Given if and only if residual is
+ *            (TTT_ERR_NULL); may be residual itself (in place).
+ */
+ttt_status ttt_rms_norm_forward(int64_t rows, int32_t width, int32_t io_dtype, float eps,
+                                const void* x, const void* residual, const float* weight,
+                                void* y, void* res_out, void* hip_stream);
+
+/*
+ * The same with y in 8 bits and one scale per row, the operands of
+ * ttt_input_projection_f8:
+ *   scale[i] = max_j |y[i,j]| / 448      (1 for a row below 5.3e-36)
+ *   y8[i,j]  = y[i,j] / scale[i], rounded to nearest even
+ *   y8       [rows,width] e4m3.         scale [rows] fp32.
+ */
+ttt_status ttt_rms_norm_forward_f8(int64_t rows, int32_t width, int32_t io_dtype, float eps,
+                                   const void* x, const void* residual, const float* weight,
+                                   void* y8, float* scale, void* res_out, void* hip_stream);
+
+/* Bytes of device workspace that ttt_rms_norm_backward needs (0 for bad sizes). */
+uint64_t ttt_rms_norm_backward_workspace_bytes(int64_t rows, int32_t width);
+
+/*
+ * Backward of the RMS norm.  With xh = r / sqrt(mean(r^2) + eps), u = dy * weight:
+ *   dx      = (u - xh * mean(u * xh)) / sqrt(mean(r^2) + eps) + dr
+ *   dweight = sum over rows of dy * xh
+ *   r        [rows,width] io_dtype: the norm's input, i.e. res_out, or x
+ *            where there was no residual.
+ *   dy       [rows,width] io_dtype.     dr [rows,width] io_dtype or NULL:
+ *            the cotangent that reaches r past the norm (of res_out).
+ *   dx       [rows,width] io_dtype: the gradient of x, and of residual.
+ *   dweight  [width] fp32.
+ */
+ttt_status ttt_rms_norm_backward(int64_t rows, int32_t width, int32_t io_dtype, float eps,
+                                 const void* r, const float* weight, const void* dy,
+                                 const void* dr, void* dx, float* dweight, void* workspace,
+                                 uint64_t workspace_bytes, void* hip_stream);
+
+/*
+ * ttt_input_projection from 8-bit operands: its rows, columns, gate and
+ * outputs, with
+ *   x      [B,T,D] e4m3 standing for x * x_scale[b,t],
+ *   w_in   [3*H*d + H, D] e4m3 standing for w_in * w_scale[row].
+ *   x_scale [B,T], w_scale [3*H*d + H] fp32.
+ * The products are exact.  The sums of q, k and v are the 8-bit matrix
+ * unit's (an error of about 2^-15 of a sum's typical size, far below the
+ * rounding of the outputs); the gate's are fp32.
+ * Sizes and refusals as ttt_input_projection (D a multiple of 64); at most
+ * 2^22 output tiles of 256 rows x 128 columns (else TTT_ERR_SHAPE).
+ */
+ttt_status ttt_input_projection_f8(const ttt_params* p, int32_t d_model, const void* x,
+                                   const float* x_scale, const void* w_in,
+                                   const float* w_scale, const float* b_eta, float eta_base,
+                                   void* q, void* k, void* v, float* eta, void* hip_stream);
+
+enum { TTT_CONV_SILU = 1u << 0 };   /* act(u) = u / (1 + exp(-u)); else act(u) = u */
+
+/*
+ * Short causal convolution along T, one filter per head and feature:
+ *   y[b,h,t,f] = act(bias[h,f] + sum_{j<K} w[h,j,f] x[b,h,t-K+1+j,f])
+ * where x[b,h,-K+1..-1] is state0 (zeros if NULL).
+ *   taps     K = 2, 3 or 4; d a multiple of 8, at most 1024 (else
+ *            TTT_ERR_UNSUPPORTED); flags TTT_CONV_SILU or 0.  B*H at most
+ *            2^23 (else TTT_ERR_SHAPE).
+ *   x, y     [B,H,T,d] io_dtype.        w [H,K,d] fp32.
+ *   bias     [H,d] fp32 or NULL (zeros).
+ *   state0   [B,H,K-1,d] io_dtype or NULL.
+ *   state_out [B,H,K-1,d] io_dtype or NULL: the last K-1 inputs (of state0
+ *            and x in turn), the state0 of a continuation.
+ */
+ttt_status ttt_conv_forward(const ttt_params* p, int32_t taps, uint32_t flags, const void* x,
+                            const float* w, const float* bias, const void* state0, void* y,
+                            void* state_out, void* hip_stream);
+
+/* One token per unit (p->T = 1; x, y [B,H,d]): as ttt_conv_forward with
+ * state0 = state, and state [B,H,K-1,d] moved on in place. */
+ttt_status ttt_conv_decode_step(const ttt_params* p, int32_t taps, uint32_t flags,
+                                const void* x, const float* w, const float* bias, void* state,
+                                void* y, void* hip_stream);
+
+/* Bytes of device workspace that ttt_conv_backward needs (0 for bad parameters). */
+uint64_t ttt_conv_backward_workspace_bytes(const ttt_params* p, int32_t taps);
+
+/*
+ * Gradients of sum(dy * y) [+ sum(dstate * state_out)]; B*H times the chunks of
+ * 256 tokens at most 2^22 (else TTT_ERR_SHAPE):
+ *   dy      [B,H,T,d] io_dtype.         dstate [B,H,K-1,d] io_dtype or NULL.
+ *   dx      [B,H,T,d] io_dtype.         dw [H,K,d], dbias [H,d] fp32 (summed
+ *           over the batch; dbias also where bias is NULL).
+ *   dstate0 [B,H,K-1,d] io_dtype or NULL.
+ */
+ttt_status ttt_conv_backward(const ttt_params* p, int32_t taps, uint32_t flags, const void* x,
+                             const float* w, const float* bias, const void* state0,
+                             const void* dy, const void* dstate, void* dx, float* dw,
+                             float* dbias, void* dstate0, void* workspace,
+                             uint64_t workspace_bytes, void* hip_stream);
+
+/*
+ * Selective state space scan.  For each (batch, head) unit, with the state
+ * S [N,d] and b, c of the head's group g = h / (H/G), token by token:
+ *   S_t = exp(a[h] dt_t) S_{t-1} + dt_t b_t^T x_t
+ *   y_t = c_t S_t + d_skip[h] x_t
+ * A sequence layer of the TTT scans' shape: S takes the place of W, and what
+ * ttt_input_projection makes fits as (x, dt, b, c) = (v, eta, k, q).
+ *   groups   G: 1..H dividing H (else TTT_ERR_SHAPE).  n: N = 32, 64 or 128,
+ *            d = 64 (else TTT_ERR_UNSUPPORTED); B*H at most 2^20 (else
+ *            TTT_ERR_SHAPE).
+ *   x, y     [B,H,T,d] io_dtype.        b, c [B,G,T,N] io_dtype.
+ *   dt       [B,H,T] fp32, used as given (0 leaves the state as it was).
+ *   a        [H] fp32 (negative for a decay).   d_skip [H] fp32 or NULL (0).
+ *   state0   [B,H,N,d] fp32 or NULL (zeros).
+ *   state_out [B,H,N,d] fp32 or NULL; may be state0 itself.
+ *   workspace at least ttt_ssm_forward_workspace_bytes bytes (NULL where
+ *            that is 0).
+ * The decays and the state are fp32 (their exponents summed in fp64); the
+ * products keep at least 16 bits of every operand for bf16 data (24 for the
+ * state) and 24 for fp32 data.  Tokens are worked on in tiles of 64 (fp32
+ * data: 32): a NaN or infinity among x, b or c may reach the outputs of the
+ * whole tile it stands in, and of all later ones.
+ */
+uint64_t ttt_ssm_forward_workspace_bytes(const ttt_params* p, int32_t groups, int32_t n);
+ttt_status ttt_ssm_forward(const ttt_params* p, int32_t groups, int32_t n, const void* x,
+                           const float* dt, const float* a, const void* b, const void* c,
+                           const float* d_skip, const float* state0, void* y,
+                           float* state_out, void* workspace, uint64_t workspace_bytes,
+                           void* hip_stream);
+
+/* One token per unit (p->T = 1; x, y [B,H,d], dt [B,H], b, c [B,G,N]):
+ * state [B,H,N,d] fp32 moved on in place. */
+ttt_status ttt_ssm_decode_step(const ttt_params* p, int32_t groups, int32_t n, const void* x,
+                               const float* dt, const float* a, const void* b, const void* c,
+                               const float* d_skip, float* state, void* y, void* hip_stream);
+
+/* Bytes of device workspace that ttt_ssm_backward needs (0 for bad parameters). */
+uint64_t ttt_ssm_backward_workspace_bytes(const ttt_params* p, int32_t groups, int32_t n);
+
+/*
+ * Gradients of sum(dy * y) [+ sum(dstate * state_out)]:
+ *   dy      [B,H,T,d] io_dtype.         dstate [B,H,N,d] fp32 or NULL.
+ *   dx      [B,H,T,d], db, dc [B,G,T,N] io_dtype (db and dc summed over a
+ *           group's heads in fp32, rounded once).
+ *   ddt     [B,H,T], da [H], dd [H] fp32 (dd given if and only if d_skip is).
+ *   dstate0 [B,H,N,d] fp32 or NULL.
+ * Nothing of the forward call has to be kept: states are made again.
+ */
+ttt_status ttt_ssm_backward(const ttt_params* p, int32_t groups, int32_t n, const void* x,
+                            const float* dt, const float* a, const void* b, const void* c,
+                            const float* d_skip, const float* state0, const void* dy,
+                            const float* dstate, void* dx, float* ddt, float* da, void* db,
+                            void* dc, float* dd, float* dstate0, void* workspace,
+                            uint64_t workspace_bytes, void* hip_stream);
 
 /* TTT_ABI_VERSION of the built library. */
 int32_t ttt_abi_version(void);

@@ -15,6 +15,7 @@ TTT_ERR_ALIAS, TTT_ERR_DEVICE, TTT_ERR_ARG, TTT_ERR_TOO_LARGE = 4, 5, 6, 7
 TTT_NOALLOC_SCRATCH_BYTES = 128 << 20
 TTT_F32, TTT_BF16 = 0, 1
 TTT_NO_LN, TTT_NO_RESIDUAL, TTT_BASES_SAVED = 1, 2, 4
+TTT_CONV_SILU = 1
 
 EXPORTS = ("ttt_linear_forward", "ttt_linear_split_workspace_bytes", "ttt_linear_forward_split",
            "ttt_linear_forward_split_noalloc",
@@ -22,7 +23,13 @@ EXPORTS = ("ttt_linear_forward", "ttt_linear_split_workspace_bytes", "ttt_linear
            "ttt_linear_backward_workspace_bytes", "ttt_linear_backward",
            "ttt_mlp_backward_workspace_bytes", "ttt_mlp_backward",
            "ttt_mlp_forward", "ttt_mlp_decode_step",
-           "ttt_mlp_decode_step_compact", "ttt_input_projection", "ttt_status_string",
+           "ttt_mlp_decode_step_compact", "ttt_input_projection",
+           "ttt_rms_norm_forward", "ttt_rms_norm_forward_f8",
+           "ttt_rms_norm_backward_workspace_bytes", "ttt_rms_norm_backward",
+           "ttt_input_projection_f8", "ttt_conv_forward", "ttt_conv_decode_step",
+           "ttt_conv_backward_workspace_bytes", "ttt_conv_backward",
+           "ttt_ssm_forward_workspace_bytes", "ttt_ssm_forward", "ttt_ssm_decode_step",
+           "ttt_ssm_backward_workspace_bytes", "ttt_ssm_backward", "ttt_status_string",
            "ttt_abi_version")
 
 
@@ -87,6 +94,28 @@ def lib() -> ctypes.CDLL:
     L.ttt_input_projection.argtypes = ([ctypes.POINTER(TTTParams), ctypes.c_int32, P, P, P,
                                         ctypes.c_float] + [P] * 5)
     L.ttt_input_projection.restype = ctypes.c_int
+    PP, I32, I64, U64 = (ctypes.POINTER(TTTParams), ctypes.c_int32, ctypes.c_int64,
+                         ctypes.c_uint64)
+    norm = [I64, I32, I32, ctypes.c_float]
+    for name, args, res in (
+            ("ttt_rms_norm_forward", norm + [P] * 6, ctypes.c_int),
+            ("ttt_rms_norm_forward_f8", norm + [P] * 7, ctypes.c_int),
+            ("ttt_rms_norm_backward_workspace_bytes", [I64, I32], U64),
+            ("ttt_rms_norm_backward", norm + [P] * 7 + [U64, P], ctypes.c_int),
+            ("ttt_input_projection_f8", [PP, I32] + [P] * 5 + [ctypes.c_float] + [P] * 5,
+             ctypes.c_int),
+            ("ttt_conv_forward", [PP, I32, ctypes.c_uint32] + [P] * 7, ctypes.c_int),
+            ("ttt_conv_decode_step", [PP, I32, ctypes.c_uint32] + [P] * 6, ctypes.c_int),
+            ("ttt_conv_backward_workspace_bytes", [PP, I32], U64),
+            ("ttt_conv_backward", [PP, I32, ctypes.c_uint32] + [P] * 11 + [U64, P],
+             ctypes.c_int),
+            ("ttt_ssm_forward_workspace_bytes", [PP, I32, I32], U64),
+            ("ttt_ssm_forward", [PP, I32, I32] + [P] * 10 + [U64, P], ctypes.c_int),
+            ("ttt_ssm_decode_step", [PP, I32, I32] + [P] * 9, ctypes.c_int),
+            ("ttt_ssm_backward_workspace_bytes", [PP, I32, I32], U64),
+            ("ttt_ssm_backward", [PP, I32, I32] + [P] * 17 + [U64, P], ctypes.c_int)):
+        getattr(L, name).argtypes = args
+        getattr(L, name).restype = res
     L.ttt_status_string.argtypes = [ctypes.c_int]
     L.ttt_status_string.restype = ctypes.c_char_p
     L.ttt_abi_version.argtypes = []

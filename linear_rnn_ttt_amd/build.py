@@ -1,7 +1,7 @@
 """Build the gfx950 C-ABI library ``libttt_amd.so`` in-tree with hipcc.
 
 The library holds the HIP kernels (csrc/*.hip) and the host entry points of
-include/ttt.h (csrc/ttt_api.cpp).  It is always built for gfx950 only.
+include/ttt.h (csrc/ttt_api.cpp, csrc/ttt_block_api.cpp).  It is always built for gfx950 only.
 """
 from __future__ import annotations
 
@@ -15,7 +15,9 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libttt_amd.so")
 SOURCES = ["ttt_api.cpp", "ttt_validate.cpp", "ttt_linear.hip", "ttt_mlp.hip", "ttt_decode.hip", "ttt_decode_compact.hip", "ttt_backward.hip",
            "ttt_mlp_decode.hip",
-           "ttt_mlp_decode_compact.hip", "ttt_mlp_backward.hip", "ttt_input.hip"]
+           "ttt_mlp_decode_compact.hip", "ttt_mlp_backward.hip", "ttt_input.hip",
+           "ttt_block_api.cpp", "ttt_block_validate.cpp", "ttt_norm.hip", "ttt_input_f8.hip",
+           "ttt_conv.hip", "ttt_ssm.hip", "ttt_ssm_backward.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 # Packed fp32 VALU instructions are disabled on purpose: the kernels are

@@ -1,0 +1,333 @@
+// ttt_ssm.hip -- the selective state space scan for gfx950: forward over
+// prompts, and the one-token step.
+//
+// Per (batch, head) unit, with the state S [N, 64], b and c of the head's group:
+//     S_t = exp(a dt_t) S_{t-1} + dt_t b_t^T x_t,   y_t = c_t S_t + d x_t
+// For a tile of L tokens, with cum_t the sum of a dt over the tile up to t and
+// S the state before it, the recurrence becomes products for the matrix unit:
+//     M[t, s] = (c_t . b_s) exp(cum_t - cum_s) dt_s  for s <= t, else 0
+//     Y  = M X + diag(exp(cum_t)) C S (+ d X)
+//     S' = exp(cum_L) S + B^T diag(exp(cum_L - cum_s) dt_s) X
+// The kernel computes the transposes Y^T = X^T M^T + S^T C^T, so that M^T
+// (from B C^T) and S leave one product in the registers as operands of the
+// next; X and B are read transposed from LDS by the transposing read.
+//
+// A workgroup of four waves walks its tiles with S in registers: wave w owns
+// features 16 w .. 16 w + 15 of x, y and S.  The blocks of M are shared out
+// over the waves and exchanged through LDS.  The next tile is fetched while
+// this one is worked on.
+//
+// Few units leave compute units idle and make a long chain of tiles, so a
+// unit's tokens are cut into segments: ttt_ssm_states_k finds what each
+// segment adds to a state of zero, ttt_ssm_join_k runs the recurrence over
+// the segments (in place), and ttt_ssm_scan_k starts every segment from its
+// own state.  With one segment only the last runs.
+//
+// Precision: bf16 data enter the products exactly; M and S in two bf16 parts
+// (16 bits, so that y keeps only its own rounding), what enters the state in
+// three (24 bits).  fp32 data are three parts throughout.
+#include "ttt_block.hpp"
+#include "ttt_block_io.hpp"
+#include "ttt_ssm_tile.hpp"
+
+namespace tttk {
+namespace {
+
+constexpr int NT = SSM_NT, P = SSM_P;
+
+// ---- what each segment adds to a state of zero ------------------------------
+
+template <int NI, int N>
+struct StatesLds {
+  static constexpr int L = kSsmTile<NI>;
+  Plane<NI, L, P> x;
+  Plane<NI, L, N> b;
+  Tokens<L> tk;
+  float fade;
+};
+
+template <int NI, int N>
+__global__ __launch_bounds__(NT) void ttt_ssm_states_k(SsmArgs a) {
+  constexpr int L = kSsmTile<NI>;
+  __shared__ alignas(16) StatesLds<NI, N> lds;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, c = lane & 15;
+  const int seg = blockIdx.x % a.segs;
+  const size_t unit = blockIdx.x / a.segs;
+  const int h = static_cast<int>(unit % a.H);
+  const size_t shared = unit / a.H * a.G + h / (a.H / a.G);
+  const int tiles = (a.T + L - 1) / L;
+  const int first = seg * a.seg_tiles, end = min(first + a.seg_tiles, tiles);
+  const float ah = a.a[h];
+  f32x4 S[N / 16];
+#pragma unroll
+  for (int i = 0; i < N / 16; ++i) S[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  Fetch<NI, L, P, NT> fx;
+  Fetch<NI, L, N, NT> fb;
+  float step = 0.f;
+  auto fetch = [&](int tile) {
+    const int t0 = tile * L, valid = min(L, a.T - t0);
+    fx.load(row_ptr<NI>(a.x, unit * a.T + t0, P), valid, tid);
+    fb.load(row_ptr<NI>(a.b, shared * a.T + t0, N), valid, tid);
+    step = lane < valid ? a.dt[unit * a.T + t0 + lane] : 0.f;
+  };
+  double total = 0.0;
+  fetch(first);
+  for (int tile = first; tile < end; ++tile) {
+    fx.store(lds.x, tid);
+    fb.store(lds.b, tid);
+    if (wave == 0) {
+      const double all = lds.tk.fill(step, ah, lane);
+      total += all;
+      if (lane == 0) lds.fade = exp2_raw(static_cast<float>(all));
+    }
+    lds_barrier();
+    if (tile + 1 < end) fetch(tile + 1);
+    add_tile<NI, L, N>(
+        S, lds.b, lds.x, lds.fade, [&](int t) { return lds.tk.into_state(t); }, wave, g, c);
+    lds_barrier();
+  }
+  float* out = a.ws_state + (unit * a.segs + seg) * (N * P);
+#pragma unroll
+  for (int i = 0; i < N / 16; ++i)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) out[(16 * i + 4 * g + r) * P + 16 * wave + c] = S[i][r];
+  if (tid == 0) a.ws_fade[unit * a.segs + seg] = total;
+}
+
+// ws_state[seg]: from what the segment adds to the state in front of it.
+__global__ __launch_bounds__(NT) void ttt_ssm_join_k(SsmArgs a) {
+  const int per = a.N * P / 4;   // 16-byte vectors of a state: a multiple of NT
+  const uint64_t i = static_cast<uint64_t>(blockIdx.x) * NT + threadIdx.x;
+  const size_t unit = i / per;
+  const size_t at = (i - unit * per) * 4;
+  const size_t size = static_cast<size_t>(a.N) * P;
+  f32x4 S = {0.f, 0.f, 0.f, 0.f};
+  if (a.state0) S = *reinterpret_cast<const f32x4*>(a.state0 + unit * size + at);
+  for (int s = 0; s < a.segs; ++s) {
+    float* p = a.ws_state + (unit * a.segs + s) * size + at;
+    const f32x4 added = *reinterpret_cast<const f32x4*>(p);
+    *reinterpret_cast<f32x4*>(p) = S;
+    S = S * exp2_raw(static_cast<float>(a.ws_fade[unit * a.segs + s])) + added;
+  }
+}
+
+// ---- the scan ---------------------------------------------------------------
+
+template <int NI, int N>
+struct ScanLds {
+  static constexpr int L = kSsmTile<NI>, TB = L / 16, BLOCKS = TB * (TB + 1) / 2;
+  static constexpr int NM = NI == 1 ? 2 : 3;   // parts of M and of S
+  Plane<NI, L, P> x;
+  Plane<NI, L, N> b, c;
+  Tokens<L> tk;
+  float fade;
+  Blocks<NM, BLOCKS> m;     // M^T: rows s, columns t
+};
+
+template <int NI, int N>
+__global__ __launch_bounds__(NT) void ttt_ssm_scan_k(SsmArgs a) {
+  using Lds = ScanLds<NI, N>;
+  constexpr int L = Lds::L, TB = Lds::TB, NM = Lds::NM;
+  __shared__ alignas(16) Lds lds;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, c = lane & 15;
+  const int seg = blockIdx.x % a.segs;
+  const size_t unit = blockIdx.x / a.segs;
+  const int h = static_cast<int>(unit % a.H);
+  const size_t shared = unit / a.H * a.G + h / (a.H / a.G);
+  const int tiles = (a.T + L - 1) / L;
+  const int first = seg * a.seg_tiles, end = min(first + a.seg_tiles, tiles);
+  const float ah = a.a[h], skip = a.d_skip ? a.d_skip[h] : 0.f;
+  f32x4 S[N / 16];
+  const float* from = a.segs > 1 ? a.ws_state + (unit * a.segs + seg) * (N * P)
+                                 : a.state0 ? a.state0 + unit * (N * P) : nullptr;
+#pragma unroll
+  for (int i = 0; i < N / 16; ++i)
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      S[i][r] = from ? from[(16 * i + 4 * g + r) * P + 16 * wave + c] : 0.f;
+  Fetch<NI, L, P, NT> fx;
+  Fetch<NI, L, N, NT> fb, fc;
+  float step = 0.f;
+  auto fetch = [&](int tile) {
+    const int t0 = tile * L, valid = min(L, a.T - t0);
+    fx.load(row_ptr<NI>(a.x, unit * a.T + t0, P), valid, tid);
+    fb.load(row_ptr<NI>(a.b, shared * a.T + t0, N), valid, tid);
+    fc.load(row_ptr<NI>(a.c, shared * a.T + t0, N), valid, tid);
+    step = lane < valid ? a.dt[unit * a.T + t0 + lane] : 0.f;
+  };
+  fetch(first);
+  for (int tile = first; tile < end; ++tile) {
+    const int t0 = tile * L, valid = min(L, a.T - t0);
+    fx.store(lds.x, tid);
+    fb.store(lds.b, tid);
+    fc.store(lds.c, tid);
+    if (wave == 0) {
+      const double all = lds.tk.fill(step, ah, lane);
+      if (lane == 0) lds.fade = exp2_raw(static_cast<float>(all));
+    }
+    lds_barrier();
+    if (tile + 1 < end) fetch(tile + 1);
+
+    // M^T block by block: (b_s . c_t), decayed and masked
+    for (int i = wave; i < Lds::BLOCKS; i += 4) {
+      int tb, sb;
+      block_of(i, &tb, &sb);
+      f32x4 m = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < N / 32; ++k)
+        m = mfma_parts(lds.b.rows8(16 * sb, 32 * k, g, c), lds.c.rows8(16 * tb, 32 * k, g, c), m);
+      const int t = 16 * tb + c;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int s = 16 * sb + 4 * g + r;
+        m[r] = s <= t ? m[r] * (lds.tk.fade(t, s) * lds.tk.dt[s]) : 0.f;
+      }
+      lds.m.put(i, lane, m);
+    }
+
+    // Y^T of the wave's features: from the state in front of the tile
+    f32x4 y[TB];
+#pragma unroll
+    for (int j = 0; j < TB; ++j) y[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < N / 32; ++k) {
+      const Parts<NM> sp = split_frag<NM>(S[2 * k], S[2 * k + 1]);
+#pragma unroll
+      for (int j = 0; j < TB; ++j)
+        y[j] = mfma_parts(sp, lds.c.rows(16 * j, 32 * k, g, c), y[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < TB; ++j) y[j] *= lds.tk.head[16 * j + c];
+    lds_barrier();
+
+    // and from the tile's own tokens
+#pragma unroll
+    for (int k = 0; k < L / 32; ++k) {
+      const Parts<NI> xs = lds.x.cols(32 * k, 16 * wave, g, c);
+#pragma unroll
+      for (int j = 2 * k; j < TB; ++j) {
+        Parts<NM> m;
+#pragma unroll
+        for (int p = 0; p < NM; ++p) {
+          const int i = j * (j + 1) / 2 + 2 * k;
+          m.p[p] = cat(lds.m.v[i][p][lane],
+                       j > 2 * k ? lds.m.v[i + 1][p][lane] : u32x2{0u, 0u});
+        }
+        y[j] = mfma_parts(xs, m, y[j]);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < TB; ++j) {
+      const int t = 16 * j + c;
+      if (a.d_skip) y[j] += lds.x.four(t, 16 * wave + 4 * g) * skip;
+      if (t < valid) {
+        const size_t at = (unit * a.T + t0 + t) * P + 16 * wave + 4 * g;
+        if constexpr (NI == 1)
+          *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.y) + at) =
+              u32x2{pack_bf16(y[j][0], y[j][1]), pack_bf16(y[j][2], y[j][3])};
+        else
+          *reinterpret_cast<f32x4*>(static_cast<float*>(a.y) + at) = y[j];
+      }
+    }
+    add_tile<NI, L, N>(
+        S, lds.b, lds.x, lds.fade, [&](int t) { return lds.tk.into_state(t); }, wave, g, c);
+    lds_barrier();
+  }
+  if (a.state_out && end == tiles) {
+    float* out = a.state_out + unit * (N * P);
+#pragma unroll
+    for (int i = 0; i < N / 16; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) out[(16 * i + 4 * g + r) * P + 16 * wave + c] = S[i][r];
+  }
+}
+
+// ---- one token --------------------------------------------------------------
+
+// A workgroup per unit: thread (row n mod 16, features 4 j .. 4 j + 3) walks
+// the state's rows 16 apart.  Bound by HBM: the state is read and written once.
+template <bool BF16, int N>
+__global__ __launch_bounds__(NT) void ttt_ssm_step_k(SsmArgs a) {
+  __shared__ float part[16][P + 4];
+  const int tid = threadIdx.x, row = tid >> 4, f = 4 * (tid & 15);
+  const size_t unit = blockIdx.x;
+  const int h = static_cast<int>(unit % a.H);
+  const size_t shared = unit / a.H * a.G + h / (a.H / a.G);
+  float* S = a.state_out + unit * (N * P);
+  f32x4 s[N / 16];
+#pragma unroll
+  for (int i = 0; i < N / 16; ++i)
+    s[i] = *reinterpret_cast<const f32x4*>(S + (16 * i + row) * P + f);
+  auto io = [](const void* p, size_t i) {
+    return BF16 ? bf16_lo_to_f32(static_cast<const uint16_t*>(p)[i])
+                : static_cast<const float*>(p)[i];
+  };
+  float b[N / 16], c[N / 16];
+#pragma unroll
+  for (int i = 0; i < N / 16; ++i) {
+    b[i] = io(a.b, shared * N + 16 * i + row);
+    c[i] = io(a.c, shared * N + 16 * i + row);
+  }
+  const float dt = a.dt[unit], fade = expf(a.a[h] * dt);
+  f32x4 x, y = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int r = 0; r < 4; ++r) x[r] = io(a.x, unit * P + f + r);
+#pragma unroll
+  for (int i = 0; i < N / 16; ++i) {
+    s[i] = s[i] * fade + x * (dt * b[i]);
+    y += s[i] * c[i];
+    *reinterpret_cast<f32x4*>(S + (16 * i + row) * P + f) = s[i];
+  }
+  *reinterpret_cast<f32x4*>(&part[row][f]) = y;
+  lds_barrier();
+  if (tid < P) {
+    float t = 0.f;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) t += part[r][tid];
+    if (a.d_skip) t += a.d_skip[h] * io(a.x, unit * P + tid);
+    if constexpr (BF16)
+      static_cast<uint16_t*>(a.y)[unit * P + tid] =
+          static_cast<uint16_t>(pack_bf16(t, 0.f) & 0xffffu);
+    else
+      static_cast<float*>(a.y)[unit * P + tid] = t;
+  }
+}
+
+template <int NI, int N>
+hipError_t scan_launch(const SsmArgs& a, hipStream_t stream) {
+  const uint32_t units = static_cast<uint32_t>(a.B) * a.H;
+  hipError_t e;
+  if (a.segs > 1) {
+    hipLaunchKernelGGL((ttt_ssm_states_k<NI, N>), dim3(units * a.segs), dim3(NT), 0, stream, a);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    hipLaunchKernelGGL(ttt_ssm_join_k, dim3(units * (N * P / 4 / NT)), dim3(NT), 0, stream, a);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL((ttt_ssm_scan_k<NI, N>), dim3(units * a.segs), dim3(NT), 0, stream,
+                     a);
+  return hipGetLastError();
+}
+
+template <int N>
+hipError_t step_launch(const SsmArgs& a, bool bf16, hipStream_t stream) {
+  const dim3 grid(static_cast<uint32_t>(a.B) * a.H);
+  if (bf16) hipLaunchKernelGGL((ttt_ssm_step_k<true, N>), grid, dim3(NT), 0, stream, a);
+  else hipLaunchKernelGGL((ttt_ssm_step_k<false, N>), grid, dim3(NT), 0, stream, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_ssm(const SsmArgs& a, bool bf16, hipStream_t stream) {
+  if (a.N == 32) return bf16 ? scan_launch<1, 32>(a, stream) : scan_launch<3, 32>(a, stream);
+  if (a.N == 64) return bf16 ? scan_launch<1, 64>(a, stream) : scan_launch<3, 64>(a, stream);
+  return bf16 ? scan_launch<1, 128>(a, stream) : scan_launch<3, 128>(a, stream);
+}
+
+hipError_t launch_ssm_decode(const SsmArgs& a, bool bf16, hipStream_t stream) {
+  if (a.N == 32) return step_launch<32>(a, bf16, stream);
+  if (a.N == 64) return step_launch<64>(a, bf16, stream);
+  return step_launch<128>(a, bf16, stream);
+}
+
+}  // namespace tttk

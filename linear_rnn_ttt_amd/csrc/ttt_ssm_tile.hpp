@@ -1,0 +1,297 @@
+// ttt_ssm_tile.hpp -- pieces shared by the selective state space scan's
+// forward and backward kernels: tiles of tokens in LDS as bf16 parts, the
+// matrix-unit fragments read from them, products of operands in parts, and
+// the decays of a tile.
+//
+// Parts.  A value is one bf16 (bf16 data: exact) or the sum of up to three,
+// each the rounding of what the ones before leave: two carry 16 bits, three
+// 24.  A product of operands in NA and NB parts adds the part products whose
+// combined order is below max(NA, NB); what is left out is below the last
+// part's own rounding.
+//
+// Fragments (64-lane wave, g = lane / 16, c = lane % 16) of a 16x16x32
+// product are two 4-value halves: half h of lane (g, c) holds contraction
+// indices 16 h + 4 g + 0..3 of row (or column) c.  That is the layout of two
+// 16x16 accumulators stacked along their rows, so an accumulator of one
+// product is an operand of the next without leaving the registers.
+#pragma once
+
+#include "ttt_block_args.hpp"
+#include "ttt_device.hpp"
+
+namespace tttk {
+
+constexpr int SSM_P = 64;     // features of x per head
+constexpr int SSM_NT = 256;   // threads of a workgroup: four waves of 16 features
+constexpr int SSM_PAD = 8;    // bf16 added to every LDS row: 16 rows hit 16 different 16-byte banks
+
+template <int N>
+struct Parts {
+  u32x4 p[N];
+};
+
+// acc += A B with operands in parts, smallest terms first.
+template <int NA, int NB>
+__device__ __forceinline__ f32x4 mfma_parts(const Parts<NA>& a, const Parts<NB>& b, f32x4 acc) {
+  constexpr int top = NA > NB ? NA : NB;
+#pragma unroll
+  for (int o = top - 1; o >= 0; --o)
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+      if (o - i >= 0 && o - i < NB) acc = mfma32(a.p[i], b.p[o - i], acc);
+  return acc;
+}
+
+// Four fp32 in NP parts.
+template <int NP>
+__device__ __forceinline__ void split_parts(f32x4 x, u32x2 out[NP]) {
+#pragma unroll
+  for (int p = 0; p < NP; ++p) {
+    out[p].x = pack_bf16(x[0], x[1]);
+    out[p].y = pack_bf16(x[2], x[3]);
+    if (p + 1 < NP) {
+      x[0] -= bf16_lo_to_f32(out[p].x);
+      x[1] -= bf16_hi_to_f32(out[p].x);
+      x[2] -= bf16_lo_to_f32(out[p].y);
+      x[3] -= bf16_hi_to_f32(out[p].y);
+    }
+  }
+}
+
+template <int NP>
+__device__ __forceinline__ Parts<NP> split_frag(f32x4 lo, f32x4 hi) {
+  u32x2 l[NP], h[NP];
+  split_parts<NP>(lo, l);
+  split_parts<NP>(hi, h);
+  Parts<NP> r;
+#pragma unroll
+  for (int p = 0; p < NP; ++p) r.p[p] = cat(l[p], h[p]);
+  return r;
+}
+
+__device__ __forceinline__ f32x4 widen4(u32x2 w) {
+  return f32x4{bf16_lo_to_f32(w.x), bf16_hi_to_f32(w.x), bf16_lo_to_f32(w.y),
+               bf16_hi_to_f32(w.y)};
+}
+
+// One half (4 values) of a fragment in fp32: exact (the parts are disjoint).
+template <int NP>
+__device__ __forceinline__ f32x4 frag_half(const Parts<NP>& f, int h) {
+  f32x4 x = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int p = NP - 1; p >= 0; --p)
+    x += widen4(h ? u32x2{f.p[p].z, f.p[p].w} : u32x2{f.p[p].x, f.p[p].y});
+  return x;
+}
+
+// L tokens x W features as NI planes of bf16 parts.
+template <int NI, int L, int W>
+struct Plane {
+  uint16_t v[NI][L][W + SSM_PAD];
+
+  // Rows t0 + c, features f0 + {4 g .. 4 g + 3, 16 + 4 g .. 16 + 4 g + 3}.
+  __device__ __forceinline__ Parts<NI> rows(int t0, int f0, int g, int c) const {
+    Parts<NI> r;
+#pragma unroll
+    for (int p = 0; p < NI; ++p) {
+      const uint16_t* s = &v[p][t0 + c][f0 + 4 * g];
+      r.p[p] = cat(*reinterpret_cast<const u32x2*>(s), *reinterpret_cast<const u32x2*>(s + 16));
+    }
+    return r;
+  }
+  // The same rows with features f0 + 8 g .. 8 g + 7 (one 16-byte read): for
+  // products whose two operands are both read this way.
+  __device__ __forceinline__ Parts<NI> rows8(int t0, int f0, int g, int c) const {
+    Parts<NI> r;
+#pragma unroll
+    for (int p = 0; p < NI; ++p)
+      r.p[p] = *reinterpret_cast<const u32x4*>(&v[p][t0 + c][f0 + 8 * g]);
+    return r;
+  }
+  // Feature f0 + c, tokens t0 + {4 g .. 4 g + 3, 16 + 4 g .. 16 + 4 g + 3}: the
+  // transposing LDS read, in which the 16 lanes of a group fetch a 4-token x
+  // 16-feature block by rows and receive it by columns.
+  __device__ __forceinline__ Parts<NI> cols(int t0, int f0, int g, int c) const {
+    typedef short s16x4l __attribute__((ext_vector_type(4)));
+    typedef __attribute__((address_space(3))) s16x4l* lp;
+    Parts<NI> r;
+#pragma unroll
+    for (int p = 0; p < NI; ++p) {
+      const uint16_t* s = &v[p][t0 + 4 * g + (c >> 2)][f0 + 4 * (c & 3)];
+      const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)s));
+      const u32x2 hi = __builtin_bit_cast(
+          u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(s + 16 * (W + SSM_PAD))));
+      r.p[p] = cat(lo, hi);
+    }
+    return r;
+  }
+  // Four features of one token in fp32.
+  __device__ __forceinline__ f32x4 four(int t, int f) const {
+    f32x4 x = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int p = NI - 1; p >= 0; --p) x += widen4(*reinterpret_cast<const u32x2*>(&v[p][t][f]));
+    return x;
+  }
+};
+
+// A tile's rows on their way from memory: 16 bytes per vector, rows from
+// `valid` on are zero.
+template <int NI, int L, int W, int THREADS>
+struct Fetch {
+  static constexpr int VE = NI == 1 ? 8 : 4;                 // values of a 16-byte vector
+  static constexpr int VECS = L * W / VE, PER = VECS / THREADS;
+  static_assert(VECS % THREADS == 0, "whole vectors per thread");
+  u32x4 r[PER];
+
+  // src: the tile's first row ([L][W] contiguous)
+  __device__ __forceinline__ void load(const void* src, int valid, int tid) {
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      const int i = tid + THREADS * j;
+      r[j] = i * VE / W < valid ? static_cast<const u32x4*>(src)[i] : u32x4{0, 0, 0, 0};
+    }
+  }
+  __device__ __forceinline__ void store(Plane<NI, L, W>& to, int tid) const {
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      const int i = tid + THREADS * j;
+      const int row = i * VE / W, col = i * VE % W;
+      if constexpr (NI == 1) {
+        *reinterpret_cast<u32x4*>(&to.v[0][row][col]) = r[j];
+      } else {
+        u32x2 p[NI];
+        split_parts<NI>(__builtin_bit_cast(f32x4, r[j]), p);
+#pragma unroll
+        for (int k = 0; k < NI; ++k) *reinterpret_cast<u32x2*>(&to.v[k][row][col]) = p[k];
+      }
+    }
+  }
+};
+
+// Inclusive sum over the wave's lanes (DPP row shifts, then row broadcasts).
+__device__ __forceinline__ double wave_scan(double v) {
+#define TTT_SCAN_STEP(ctrl, rows)                                                           \
+  {                                                                                         \
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);                                     \
+    const uint32_t lo = static_cast<uint32_t>(__builtin_amdgcn_update_dpp(                  \
+        0, static_cast<int>(b & 0xffffffffu), ctrl, rows, 0xf, false));                     \
+    const uint32_t hi = static_cast<uint32_t>(                                              \
+        __builtin_amdgcn_update_dpp(0, static_cast<int>(b >> 32), ctrl, rows, 0xf, false)); \
+    v += __builtin_bit_cast(double, (static_cast<uint64_t>(hi) << 32) | lo);                \
+  }
+  TTT_SCAN_STEP(0x111, 0xf)   // row_shr 1, 2, 4, 8: within 16 lanes
+  TTT_SCAN_STEP(0x112, 0xf)
+  TTT_SCAN_STEP(0x114, 0xf)
+  TTT_SCAN_STEP(0x118, 0xf)
+  TTT_SCAN_STEP(0x142, 0xa)   // row_bcast 15: rows 1 and 3 take their left row's total
+  TTT_SCAN_STEP(0x143, 0xc)   // row_bcast 31: rows 2 and 3 take the first half's total
+#undef TTT_SCAN_STEP
+  return v;
+}
+
+__device__ __forceinline__ double last_lane(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(b & 0xffffffffu), 63);
+  const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(b >> 32), 63);
+  return __builtin_bit_cast(double, (static_cast<uint64_t>(hi) << 32) | lo);
+}
+
+__device__ __forceinline__ float exp2_raw(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// Per-token values of a tile.  cum_t = log2(e) a (dt_0 + ... + dt_t) is summed
+// in fp64 and kept as hi + lo, so that a difference of two of them keeps
+// fp32's relative precision also behind a large step that resets the state.
+template <int L>
+struct alignas(16) Tokens {
+  float hi[L], lo[L];   // cum
+  float dt[L];
+  float head[L];        // exp2(cum_t): from the tile's start through token t
+  float tail[L];        // exp2(cum_last - cum_t): from token t to the tile's end
+
+  // By one wave; lane = token, dt = 0 from the tile's valid tokens on.
+  // Returns log2 of the whole tile's decay.
+  __device__ __forceinline__ double fill(float step, float a, int lane) {
+    constexpr double LOG2E = 1.4426950408889634074;
+    const double cum = wave_scan(static_cast<double>(step) * (static_cast<double>(a) * LOG2E));
+    const double all = last_lane(cum);
+    if (lane < L) {
+      const float h = static_cast<float>(cum);
+      hi[lane] = h;
+      lo[lane] = static_cast<float>(cum - static_cast<double>(h));
+      dt[lane] = step;
+      head[lane] = exp2_raw(h);
+      tail[lane] = exp2_raw(static_cast<float>(all - cum));
+    }
+    return all;
+  }
+  // of tokens t .. t + 3: what the input of each weighs in the state behind
+  // the tile, and what the state in front of it weighs at each
+  __device__ __forceinline__ f32x4 into_state(int t) const {
+    return *reinterpret_cast<const f32x4*>(&tail[t]) * *reinterpret_cast<const f32x4*>(&dt[t]);
+  }
+  __device__ __forceinline__ f32x4 from_state(int t) const {
+    return *reinterpret_cast<const f32x4*>(&head[t]);
+  }
+  // exp of the decay exponents summed over tokens s+1 .. t
+  __device__ __forceinline__ float fade(int t, int s) const {
+    return exp2_raw((hi[t] - hi[s]) + (lo[t] - lo[s]));
+  }
+};
+
+// The tokens x tokens blocks on and below the diagonal, in order of t then s:
+// block index of (tb, sb) = tb (tb + 1) / 2 + sb.
+__device__ __forceinline__ void block_of(int i, int* tb, int* sb) {
+  int t = 0;
+  while (i > t) {
+    i -= t + 1;
+    ++t;
+  }
+  *tb = t;
+  *sb = i;
+}
+
+// One wave's 16x16 block of a tokens x tokens matrix as an operand: lane's
+// four values (rows 4 g + 0..3) in NP parts, at the lane's own place.
+template <int NP, int BLOCKS>
+struct Blocks {
+  u32x2 v[BLOCKS][NP][64];
+
+  __device__ __forceinline__ void put(int i, int lane, f32x4 x) {
+    u32x2 p[NP];
+    split_parts<NP>(x, p);
+#pragma unroll
+    for (int k = 0; k < NP; ++k) v[i][k][lane] = p[k];
+  }
+};
+
+template <int NI>
+constexpr int kSsmTile = NI == 1 ? 64 : 32;
+
+template <int NI>
+__device__ __forceinline__ const char* row_ptr(const void* p, size_t row, int width) {
+  return static_cast<const char*>(p) + row * width * (NI == 1 ? 2 : 4);
+}
+
+// S = fade S + B^T diag(w) X over a tile: rows n of S from A = B^T, the wave's
+// 16 features from the weighted X, in three parts.  weight(t) gives the
+// weights of tokens t .. t + 3.
+template <int NI, int L, int N, class Weight>
+__device__ __forceinline__ void add_tile(f32x4 (&S)[N / 16], const Plane<NI, L, N>& b,
+                                         const Plane<NI, L, SSM_P>& x, float fade, Weight weight,
+                                         int wave, int g, int c) {
+#pragma unroll
+  for (int i = 0; i < N / 16; ++i) S[i] *= fade;
+#pragma unroll
+  for (int k = 0; k < L / 32; ++k) {
+    const Parts<NI> xs = x.cols(32 * k, 16 * wave, g, c);
+    f32x4 w[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) w[h] = frag_half(xs, h) * weight(32 * k + 16 * h + 4 * g);
+    const Parts<3> xw = split_frag<3>(w[0], w[1]);
+#pragma unroll
+    for (int i = 0; i < N / 16; ++i)
+      S[i] = mfma_parts(b.cols(32 * k, 16 * i, g, c), xw, S[i]);
+  }
+}
+
+}  // namespace tttk
