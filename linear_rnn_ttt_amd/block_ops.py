@@ -14,7 +14,7 @@ from typing import Optional, Tuple
 import torch
 
 from . import _lib
-from .ops import HEAD_DIM, _dev_tensor, _ptr, _stream
+from .ops import HEAD_DIM, _dev_tensor
 
 __all__ = ["ttt_rms_norm_forward", "ttt_rms_norm_forward_f8", "ttt_rms_norm_backward",
            "ttt_input_projection_f8", "ttt_conv_forward", "ttt_conv_decode_step",
@@ -22,33 +22,61 @@ __all__ = ["ttt_rms_norm_forward", "ttt_rms_norm_forward_f8", "ttt_rms_norm_back
 
 F8 = torch.float8_e4m3fn
 
+# the handle of a device's current stream, without a Stream object around it
+# where this torch has that
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+# The host side of a call is what a launch of a few microseconds waits for, so
+# a good argument costs one line of comparisons; only one that fails them goes
+# through _dev_tensor, which finds out why and raises.
+
+def _check(name, t, dtype, shape, device):
+    try:
+        if (t.dtype is dtype and t.shape == shape and t.device == device
+                and t.is_contiguous()):
+            return t
+    except AttributeError:
+        pass
+    return _dev_tensor(name, t, dtype, shape, device)
+
 
 def _io(name, t) -> int:
-    _dev_tensor(name, t)
-    if t.dtype == torch.bfloat16:
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.is_contiguous()):
+        _dev_tensor(name, t)
+    if t.dtype is torch.bfloat16:
         return _lib.TTT_BF16
-    if t.dtype == torch.float32:
+    if t.dtype is torch.float32:
         return _lib.TTT_F32
     raise ValueError("%s must be bfloat16 or float32 (got %s)" % (name, t.dtype))
 
 
 def _optional(name, t, dtype, shape, device):
     if t is not None:
-        _dev_tensor(name, t, dtype, shape, device)
-    return t
+        _check(name, t, dtype, shape, device)
 
 
-def _given(name, t, like_shape, dtype, device):
+def _given(name, t, shape, dtype, device):
     """An output: the caller's tensor, checked, or a new one."""
     if t is None:
-        return torch.empty(like_shape, dtype=dtype, device=device)
-    return _dev_tensor(name, t, dtype, like_shape, device)
+        return torch.empty(shape, dtype=dtype, device=device)
+    return _check(name, t, dtype, shape, device)
+
+
+def _like(name, t, x):
+    """As _given, of x's shape and type."""
+    return torch.empty_like(x) if t is None else _check(name, t, x.dtype, x.shape, x.device)
 
 
 def _workspace(ws, need, device):
     if ws is None:
-        return torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+        return torch.empty(need or 1, dtype=torch.uint8, device=device)
     return _dev_tensor("workspace", ws, torch.uint8, device=device)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _on_stream(func):
@@ -62,9 +90,16 @@ def _on_stream(func):
 
 
 def _call(func, device, *args):
-    with torch.cuda.device(device):   # the library launches on the current device
-        rc = getattr(_lib.lib(), func)(*args)
-    _lib.check(func, rc)
+    """The library's function on the device's current stream; it launches on
+    the current device."""
+    index = device.index
+    if index == torch.cuda.current_device():
+        rc = getattr(_lib.lib(), func)(*args, _current_stream(index))
+    else:
+        with torch.cuda.device(device):
+            rc = getattr(_lib.lib(), func)(*args, _current_stream(index))
+    if rc:
+        _lib.check(func, rc)
 
 
 # ---- RMS norm ---------------------------------------------------------------
@@ -76,13 +111,13 @@ def _norm_args(x, weight, residual, res_out):
     width = x.shape[-1]
     rows = x.numel() // width if width else 0
     dev = x.device
-    _dev_tensor("weight", weight, torch.float32, (width,), dev)
+    _check("weight", weight, torch.float32, (width,), dev)
     _optional("residual", residual, x.dtype, x.shape, dev)
     if residual is None:
         if res_out is not None:
             raise ValueError("res_out is given without a residual")
     else:
-        res_out = _given("res_out", res_out, x.shape, x.dtype, dev)
+        res_out = _like("res_out", res_out, x)
     return io, rows, width, res_out
 
 
@@ -90,16 +125,15 @@ def _norm_args(x, weight, residual, res_out):
 def ttt_rms_norm_forward(x: torch.Tensor, weight: torch.Tensor,
                          residual: Optional[torch.Tensor] = None, *, eps: float = 1e-6,
                          y: Optional[torch.Tensor] = None,
-                         res_out: Optional[torch.Tensor] = None, stream=None
-                         ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+                         res_out: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """RMS norm over the last dimension of x [..., width] (bf16 or fp32) after
     adding residual; returns (y, r) with r = x + residual in x's type, or None
     without a residual.  weight [width] fp32; width a multiple of 8.
     res_out: where to write r (may be residual itself)."""
     io, rows, width, res_out = _norm_args(x, weight, residual, res_out)
-    y = _given("y", y, x.shape, x.dtype, x.device)
+    y = _like("y", y, x)
     _call("ttt_rms_norm_forward", x.device, rows, width, io, float(eps), _ptr(x), _ptr(residual),
-          _ptr(weight), _ptr(y), _ptr(res_out), _stream(x, stream))
+          _ptr(weight), _ptr(y), _ptr(res_out))
     return y, res_out
 
 
@@ -117,7 +151,7 @@ def ttt_rms_norm_forward_f8(x: torch.Tensor, weight: torch.Tensor,
     y = _given("y", y, x.shape, F8, x.device)
     scale = _given("scale", scale, x.shape[:-1], torch.float32, x.device)
     _call("ttt_rms_norm_forward_f8", x.device, rows, width, io, float(eps), _ptr(x),
-          _ptr(residual), _ptr(weight), _ptr(y), _ptr(scale), _ptr(res_out), _stream(x, stream))
+          _ptr(residual), _ptr(weight), _ptr(y), _ptr(scale), _ptr(res_out))
     return y, scale, res_out
 
 
@@ -138,16 +172,15 @@ def ttt_rms_norm_backward(r: torch.Tensor, weight: torch.Tensor, dy: torch.Tenso
         raise ValueError("r must be [..., width]")
     dev, width = r.device, r.shape[-1]
     rows = r.numel() // width if width else 0
-    _dev_tensor("weight", weight, torch.float32, (width,), dev)
-    _dev_tensor("dy", dy, r.dtype, r.shape, dev)
+    _check("weight", weight, torch.float32, (width,), dev)
+    _check("dy", dy, r.dtype, r.shape, dev)
     _optional("dr", dr, r.dtype, r.shape, dev)
-    dx = _given("dx", dx, r.shape, r.dtype, dev)
+    dx = _like("dx", dx, r)
     dweight = _given("dweight", dweight, (width,), torch.float32, dev)
     need = int(_lib.lib().ttt_rms_norm_backward_workspace_bytes(rows, width))
     workspace = _workspace(workspace, need, dev)
     _call("ttt_rms_norm_backward", dev, rows, width, io, float(eps), _ptr(r), _ptr(weight),
-          _ptr(dy), _ptr(dr), _ptr(dx), _ptr(dweight), _ptr(workspace), workspace.numel(),
-          _stream(r, stream))
+          _ptr(dy), _ptr(dr), _ptr(dx), _ptr(dweight), _ptr(workspace), workspace.numel())
     return dx, dweight
 
 
@@ -170,10 +203,10 @@ def ttt_input_projection_f8(x: torch.Tensor, x_scale: torch.Tensor, w_in: torch.
     B, T, D = x.shape
     H, d, dev = int(heads), int(head_dim), x.device
     n = 3 * H * d + H
-    _dev_tensor("x_scale", x_scale, torch.float32, (B, T), dev)
-    _dev_tensor("w_in", w_in, F8, (n, D), dev)
-    _dev_tensor("w_scale", w_scale, torch.float32, (n,), dev)
-    _dev_tensor("b_eta", b_eta, torch.float32, (H,), dev)
+    _check("x_scale", x_scale, torch.float32, (B, T), dev)
+    _check("w_in", w_in, F8, (n, D), dev)
+    _check("w_scale", w_scale, torch.float32, (n,), dev)
+    _check("b_eta", b_eta, torch.float32, (H,), dev)
     if out is None:
         out = (None,) * 4
     q, k, v = (_given(name, t, (B, H, T, d), torch.bfloat16, dev)
@@ -181,8 +214,7 @@ def ttt_input_projection_f8(x: torch.Tensor, x_scale: torch.Tensor, w_in: torch.
     eta = _given("eta", out[3], (B, H, T), torch.float32, dev)
     p = _lib.TTTParams(B, H, T, d, 16, _lib.TTT_BF16, 0, 0.0, 0)
     _call("ttt_input_projection_f8", dev, ctypes.byref(p), D, _ptr(x), _ptr(x_scale), _ptr(w_in),
-          _ptr(w_scale), _ptr(b_eta), float(eta_base), _ptr(q), _ptr(k), _ptr(v), _ptr(eta),
-          _stream(x, stream))
+          _ptr(w_scale), _ptr(b_eta), float(eta_base), _ptr(q), _ptr(k), _ptr(v), _ptr(eta))
     return q, k, v, eta
 
 
@@ -216,12 +248,11 @@ def ttt_conv_forward(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tens
     before the first token (zeros if None)."""
     p, taps, tail = _conv_args(x, w, bias, 4)
     _optional("state0", state0, x.dtype, tail, x.device)
-    y = _given("y", y, x.shape, x.dtype, x.device)
+    y = _like("y", y, x)
     if state_out is not None or return_state:
         state_out = _given("state_out", state_out, tail, x.dtype, x.device)
     _call("ttt_conv_forward", x.device, ctypes.byref(p), taps, _lib.TTT_CONV_SILU if silu else 0,
-          _ptr(x), _ptr(w), _ptr(bias), _ptr(state0), _ptr(y), _ptr(state_out),
-          _stream(x, stream))
+          _ptr(x), _ptr(w), _ptr(bias), _ptr(state0), _ptr(y), _ptr(state_out))
     return y, state_out
 
 
@@ -232,11 +263,10 @@ def ttt_conv_decode_step(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.
     """One token of ttt_conv_forward: x [B,H,d]; state [B,H,taps-1,d] in x's
     type holds the inputs before it and is moved on in place.  Returns y."""
     p, taps, tail = _conv_args(x, w, bias, 3)
-    _dev_tensor("state", state, x.dtype, tail, x.device)
-    y = _given("y", y, x.shape, x.dtype, x.device)
+    _check("state", state, x.dtype, tail, x.device)
+    y = _like("y", y, x)
     _call("ttt_conv_decode_step", x.device, ctypes.byref(p), taps,
-          _lib.TTT_CONV_SILU if silu else 0, _ptr(x), _ptr(w), _ptr(bias), _ptr(state), _ptr(y),
-          _stream(x, stream))
+          _lib.TTT_CONV_SILU if silu else 0, _ptr(x), _ptr(w), _ptr(bias), _ptr(state), _ptr(y))
     return y
 
 
@@ -254,7 +284,7 @@ def ttt_conv_backward(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Ten
     p, taps, tail = _conv_args(x, w, bias, 4)
     dev = x.device
     _optional("state0", state0, x.dtype, tail, dev)
-    _dev_tensor("dy", dy, x.dtype, x.shape, dev)
+    _check("dy", dy, x.dtype, x.shape, dev)
     _optional("dstate", dstate, x.dtype, tail, dev)
     dx, dw = torch.empty_like(x), torch.empty_like(w)
     dbias = torch.empty((w.shape[0], w.shape[2]), dtype=torch.float32, device=dev)
@@ -263,7 +293,7 @@ def ttt_conv_backward(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Ten
     workspace = _workspace(workspace, need, dev)
     _call("ttt_conv_backward", dev, ctypes.byref(p), taps, _lib.TTT_CONV_SILU if silu else 0,
           _ptr(x), _ptr(w), _ptr(bias), _ptr(state0), _ptr(dy), _ptr(dstate), _ptr(dx), _ptr(dw),
-          _ptr(dbias), _ptr(dstate0), _ptr(workspace), workspace.numel(), _stream(x, stream))
+          _ptr(dbias), _ptr(dstate0), _ptr(workspace), workspace.numel())
     return dx, dw, dbias, dstate0
 
 
@@ -276,12 +306,12 @@ def _ssm_args(x, dt, a, b, c, d_skip, dims):
     B, H, d = x.shape[0], x.shape[1], x.shape[-1]
     t = x.shape[2:-1]
     dev = x.device
-    _dev_tensor("dt", dt, torch.float32, (B, H) + tuple(t), dev)
-    _dev_tensor("a", a, torch.float32, (H,), dev)
+    _check("dt", dt, torch.float32, (B, H) + tuple(t), dev)
+    _check("a", a, torch.float32, (H,), dev)
     _dev_tensor("b", b, x.dtype, device=dev)
     if b.dim() != dims or b.shape[0] != B or b.shape[2:-1] != t:
         raise ValueError("b must be [B, groups, T, N] beside x (got %s)" % (tuple(b.shape),))
-    _dev_tensor("c", c, x.dtype, b.shape, dev)
+    _check("c", c, x.dtype, b.shape, dev)
     _optional("d_skip", d_skip, torch.float32, (H,), dev)
     G, N = b.shape[1], b.shape[-1]
     p = _lib.TTTParams(B, H, t[0] if dims == 4 else 1, d, 16, io, 0, 0.0, 0)
@@ -306,7 +336,7 @@ def ttt_ssm_forward(x: torch.Tensor, dt: torch.Tensor, a: torch.Tensor, b: torch
     p, G, N, state = _ssm_args(x, dt, a, b, c, d_skip, 4)
     dev = x.device
     _optional("state0", state0, torch.float32, state, dev)
-    y = _given("y", y, x.shape, x.dtype, dev)
+    y = _like("y", y, x)
     if state_out is not None or return_state:
         state_out = _given("state_out", state_out, state, torch.float32, dev)
     if workspace is None:
@@ -316,7 +346,7 @@ def ttt_ssm_forward(x: torch.Tensor, dt: torch.Tensor, a: torch.Tensor, b: torch
         _dev_tensor("workspace", workspace, torch.uint8, device=dev)
     _call("ttt_ssm_forward", dev, ctypes.byref(p), G, N, _ptr(x), _ptr(dt), _ptr(a), _ptr(b),
           _ptr(c), _ptr(d_skip), _ptr(state0), _ptr(y), _ptr(state_out), _ptr(workspace),
-          0 if workspace is None else workspace.numel(), _stream(x, stream))
+          0 if workspace is None else workspace.numel())
     return y, state_out
 
 
@@ -328,10 +358,10 @@ def ttt_ssm_decode_step(x: torch.Tensor, dt: torch.Tensor, a: torch.Tensor, b: t
     """One token of ttt_ssm_forward: x [B,H,d], dt [B,H], b, c [B,G,N]; state
     [B,H,N,d] fp32 is moved on in place.  Returns y [B,H,d]."""
     p, G, N, shape = _ssm_args(x, dt, a, b, c, d_skip, 3)
-    _dev_tensor("state", state, torch.float32, shape, x.device)
-    y = _given("y", y, x.shape, x.dtype, x.device)
+    _check("state", state, torch.float32, shape, x.device)
+    y = _like("y", y, x)
     _call("ttt_ssm_decode_step", x.device, ctypes.byref(p), G, N, _ptr(x), _ptr(dt), _ptr(a),
-          _ptr(b), _ptr(c), _ptr(d_skip), _ptr(state), _ptr(y), _stream(x, stream))
+          _ptr(b), _ptr(c), _ptr(d_skip), _ptr(state), _ptr(y))
     return y
 
 
@@ -349,7 +379,7 @@ def ttt_ssm_backward(x: torch.Tensor, dt: torch.Tensor, a: torch.Tensor, b: torc
     ttt_ssm_backward_workspace_bytes bytes to use instead of a fresh one."""
     p, G, N, state = _ssm_args(x, dt, a, b, c, d_skip, 4)
     dev = x.device
-    _dev_tensor("dy", dy, x.dtype, x.shape, dev)
+    _check("dy", dy, x.dtype, x.shape, dev)
     _optional("state0", state0, torch.float32, state, dev)
     _optional("dstate", dstate, torch.float32, state, dev)
     dx, db, dc = torch.empty_like(x), torch.empty_like(b), torch.empty_like(c)
@@ -361,5 +391,5 @@ def ttt_ssm_backward(x: torch.Tensor, dt: torch.Tensor, a: torch.Tensor, b: torc
     _call("ttt_ssm_backward", dev, ctypes.byref(p), G, N, _ptr(x), _ptr(dt), _ptr(a), _ptr(b),
           _ptr(c), _ptr(d_skip), _ptr(state0), _ptr(dy), _ptr(dstate), _ptr(dx), _ptr(ddt),
           _ptr(da), _ptr(db), _ptr(dc), _ptr(dd), _ptr(dstate0), _ptr(workspace),
-          workspace.numel(), _stream(x, stream))
+          workspace.numel())
     return dx, ddt, da, db, dc, dd, dstate0
