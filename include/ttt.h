@@ -550,8 +550,9 @@ ttt_status ttt_rms_norm_backward(int64_t rows, int32_t width, int32_t io_dtype, 
  * The products are exact.  The sums of q, k and v are the 8-bit matrix
  * unit's (an error of about 2^-15 of a sum's typical size, far below the
  * rounding of the outputs); the gate's are fp32.
- * Sizes and refusals as ttt_input_projection (D a multiple of 64); at most
- * 2^22 output tiles of 256 rows x 128 columns (else TTT_ERR_SHAPE).
+ * Sizes and refusals as ttt_input_projection (D a multiple of 64, here at
+ * most 2^20); at most 2^23 output tiles of 128 rows x 32 columns (else
+ * TTT_ERR_SHAPE).
  */
 ttt_status ttt_input_projection_f8(const ttt_params* p, int32_t d_model, const void* x,
                                    const float* x_scale, const void* w_in,

@@ -57,6 +57,8 @@ struct ConvArgs {
   int32_t B, H, T, d, taps, silu;
 };
 
+constexpr int32_t kConvChunk = 256;   // tokens of one partial filter gradient
+
 struct ConvBackwardArgs {
   const void* x;
   const float* w;

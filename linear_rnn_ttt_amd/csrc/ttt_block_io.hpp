@@ -119,4 +119,36 @@ __device__ __forceinline__ float wave_max(float x) {
   return fmaxf(bitsf(q[0]), bitsf(q[1]));
 }
 
+// put(i, sum over `rows` of partial[row][i]) for the columns i < n of a
+// workgroup of 256 threads: 16 columns (16 blockIdx.x ..), 16 threads each,
+// every thread's rows in four interleaved sums so that their loads overlap.
+// The order is fixed, so the sums are the same from run to run.
+template <class Put>
+__device__ __forceinline__ void column_sums(const float* partial, size_t n, int64_t rows,
+                                            Put put) {
+  __shared__ float part[16][17];
+  const int col = threadIdx.x & 15, slot = threadIdx.x >> 4;
+  const size_t i = 16 * static_cast<size_t>(blockIdx.x) + col;
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
+  if (i < n) {
+    int64_t r = slot;
+    for (; r + 112 < rows; r += 128) {
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = partial[(r + 16 * k) * n + i];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s[k & 3] += v[k];
+    }
+    for (; r < rows; r += 16) s[0] += partial[r * n + i];
+  }
+  part[slot][col] = (s[0] + s[1]) + (s[2] + s[3]);
+  __syncthreads();
+  if (slot == 0 && i < n) {
+    float t = 0.f;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) t += part[k][col];
+    put(i, t);
+  }
+}
+
 }  // namespace tttk

@@ -86,7 +86,6 @@ ttt_status check_norm(int64_t rows, int32_t width, int32_t io_dtype, float eps, 
 // ---- convolution ----
 
 constexpr int32_t kConvMaxDim = 1024;
-constexpr int32_t kConvChunk = 256;        // tokens of one partial weight gradient
 
 ttt_status check_conv(const ttt_params* p, int32_t taps, uint32_t flags, uint64_t* units,
                       uint64_t* es) {
@@ -99,7 +98,9 @@ ttt_status check_conv(const ttt_params* p, int32_t taps, uint32_t flags, uint64_
   return TTT_OK;
 }
 
-int32_t conv_chunks(const ttt_params* p) { return (p->T + kConvChunk - 1) / kConvChunk; }
+int32_t conv_chunks(const ttt_params* p) {
+  return (p->T + tttk::kConvChunk - 1) / tttk::kConvChunk;
+}
 
 // ---- scan ----
 
@@ -283,15 +284,15 @@ ttt_status input_projection_f8(const ttt_params* p, int32_t d_model, const void*
   if (!x || !x_scale || !w_in || !w_scale || !b_eta || !q || !k || !v || !eta)
     return TTT_ERR_NULL;
   if (d_model < 1) return TTT_ERR_SHAPE;
-  if (p->d != kHeadDim || p->io_dtype != TTT_BF16 || d_model % 64 != 0)
+  if (p->d != kHeadDim || p->io_dtype != TTT_BF16 || d_model % 64 != 0 || d_model > (1 << 20))
     return TTT_ERR_UNSUPPORTED;
   if (!(eta_base > 0.0f) || !std::isfinite(eta_base)) return TTT_ERR_ARG;
   if (misaligned({x, w_in, q, k, v})) return TTT_ERR_ARG;
   const uint64_t tokens = static_cast<uint64_t>(p->B) * p->T;
   const uint64_t n_out = 3ull * p->H * kHeadDim + p->H;
-  // the kernel indexes rows, columns and tiles (256 rows x 128 columns) with int
+  // the kernel indexes rows, columns and tiles (128 x 128 at the smallest for many rows) with int
   if (tokens > (1ull << 30) || n_out > (1ull << 30) ||
-      ((tokens + 255) / 256) * ((n_out + 127) / 128) > kMaxWorkgroups)
+      ((tokens + 127) / 128) * ((n_out + 31) / 32) > kMaxWorkgroups * 2)
     return TTT_ERR_SHAPE;
   const uint64_t elems = units * p->T * kHeadDim;
   if (any_overlap({span(q, elems * 2), span(k, elems * 2), span(v, elems * 2),

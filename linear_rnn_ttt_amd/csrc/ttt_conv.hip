@@ -12,6 +12,8 @@
 // in registers, so x comes from HBM once; the K - 1 inputs in front of a strip
 // are the neighbouring strip's lines, in cache.  The loads of a strip are
 // issued together before any of them is used.
+#include <type_traits>
+
 #include "ttt_block.hpp"
 #include "ttt_block_io.hpp"
 
@@ -19,10 +21,14 @@ namespace tttk {
 namespace {
 
 constexpr int NT = 256;
-constexpr int S = 8;              // tokens of a strip
+constexpr int S = 8;              // tokens of a strip (4, 8, 16: forward 55, 54, 59 us, backward 27, 24, 40 us)
 constexpr uint32_t MAX_GRID = 1u << 20;
 
-__device__ __forceinline__ float sigmoid(float u) { return 1.0f / (1.0f + __expf(-u)); }
+// v_exp_f32 and v_rcp_f32, one unit each: far below what the tests' fp32 bound
+// allows, and a third of the instructions of a full division.
+__device__ __forceinline__ float sigmoid(float u) {
+  return __builtin_amdgcn_rcpf(1.0f + __expf(-u));
+}
 
 template <int K>
 struct Filter {
@@ -139,48 +145,77 @@ __global__ __launch_bounds__(NT) void ttt_conv_step_k(ConvArgs a) {
     store8<BF16>(a.state_out, (unit * (K - 1) + j) * d + f, widen8(win[j + 1]));
 }
 
-// Backward: a workgroup takes one unit's chunk of CHUNK tokens.  Threads are
-// (strip of S tokens) x (8 features); where a chunk's strips do not fit at
-// once (d > 64) they take turns.  The filter gradients are summed over a
-// thread's strips in registers, over the workgroup's strips through LDS and
-// left as one partial [K+1][d] per chunk.
-constexpr int CHUNK = 256;
+// Backward: a workgroup takes one unit's chunk of tokens.  Threads are
+// (strip of S tokens) x (4 features: with 8 the windows of x, dy and du took
+// over 256 registers and left one wave per SIMD; 38.6 -> 23.6 us at B8 H12
+// T2048); where a chunk's strips do not fit at once they take turns.  The
+// filter gradients are summed over a thread's strips in registers, over the
+// workgroup's strips through LDS and left as one partial [K+1][d] per chunk.
+constexpr int CHUNK = kConvChunk;
+
+template <bool BF16>
+using Raw4 = std::conditional_t<BF16, u32x2, f32x4>;
+
+template <bool BF16>
+__device__ __forceinline__ Raw4<BF16> load4_raw(const void* p, size_t i) {
+  return *reinterpret_cast<const Raw4<BF16>*>(static_cast<const char*>(p) + i * kIoBytes<BF16>);
+}
+template <bool BF16>
+__device__ __forceinline__ f32x4 to_f32(const Raw4<BF16>& r) {
+  if constexpr (BF16)
+    return f32x4{bf16_lo_to_f32(r.x), bf16_hi_to_f32(r.x), bf16_lo_to_f32(r.y),
+                 bf16_hi_to_f32(r.y)};
+  else
+    return r;
+}
+template <bool BF16>
+__device__ __forceinline__ void store4(void* p, size_t i, f32x4 v) {
+  if constexpr (BF16)
+    *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(p) + i) =
+        u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+  else
+    *reinterpret_cast<f32x4*>(static_cast<float*>(p) + i) = v;
+}
 
 template <bool BF16, int K>
 __global__ __launch_bounds__(NT) void ttt_conv_bwd_k(ConvBackwardArgs a) {
-  __shared__ float red[NT][9];
+  __shared__ float red[K + 1][4][NT + 1];
   const int T = a.T, d = a.d;
-  const int lanes = d / 8, rows = NT / lanes;       // d <= 1024: lanes <= 128
+  const int lanes = d / 4, rows = NT / lanes;       // d <= 1024: lanes <= 256
   const size_t unit = blockIdx.x / a.chunks;
   const int chunk = blockIdx.x - static_cast<uint32_t>(unit) * a.chunks;
   const int h = static_cast<int>(unit % a.H), b = static_cast<int>(unit / a.H);
-  const int row = threadIdx.x / lanes, f = 8 * (threadIdx.x - row * lanes);
-  F8 acc[K + 1];
+  const int row = threadIdx.x / lanes, f = 4 * (threadIdx.x - row * lanes);
+  const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+  auto input = [&](int t) {   // as input_at
+    if (t >= 0) return t < T ? load4_raw<BF16>(a.x, (unit * T + t) * d + f) : Raw4<BF16>{};
+    return a.state0 ? load4_raw<BF16>(a.state0, (unit * (K - 1) + (t + K - 1)) * d + f)
+                    : Raw4<BF16>{};
+  };
+  f32x4 acc[K + 1];
 #pragma unroll
-  for (int j = 0; j <= K; ++j)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) acc[j].v[e] = 0.f;
+  for (int j = 0; j <= K; ++j) acc[j] = zero;
   if (row < rows) {
-    const Filter<K> flt = load_filter<K>(a.w, a.bias, h, d, f);
+    f32x4 w[K], bias = zero;
+#pragma unroll
+    for (int j = 0; j < K; ++j)
+      w[j] = *reinterpret_cast<const f32x4*>(a.w + (static_cast<size_t>(h) * K + j) * d + f);
+    if (a.bias) bias = *reinterpret_cast<const f32x4*>(a.bias + static_cast<size_t>(h) * d + f);
     for (int strip = row; strip < CHUNK / S; strip += rows) {
       const int t0 = chunk * CHUNK + strip * S;
       if (t0 >= T) break;
       // inputs t0-K+1 .. t0+S+K-2 and cotangents t0 .. t0+S+K-2
-      Raw8<BF16> in8[S + 2 * (K - 1)], g8[S + K - 1];
+      Raw4<BF16> in[S + 2 * (K - 1)], g[S + K - 1];
 #pragma unroll
-      for (int s = 0; s < S + 2 * (K - 1); ++s)
-        in8[s] = input_at<BF16, K>(a.x, a.state0, unit, t0 + s - (K - 1), T, d, f);
+      for (int s = 0; s < S + 2 * (K - 1); ++s) in[s] = input(t0 + s - (K - 1));
 #pragma unroll
       for (int s = 0; s < S + K - 1; ++s)
-        g8[s] = t0 + s < T ? load8_raw<BF16>(a.dy, (unit * T + t0 + s) * d + f)
-                           : zero8_raw<BF16>();
-      F8 win[K], dus[K];   // dus[j] = du of token (current - (K-1) + j)
+        g[s] = t0 + s < T ? load4_raw<BF16>(a.dy, (unit * T + t0 + s) * d + f) : Raw4<BF16>{};
+      f32x4 win[K], dus[K];   // dus[j] = du of token (current - (K-1) + j)
 #pragma unroll
-      for (int j = 0; j < K - 1; ++j) win[j + 1] = widen8(in8[j]);
+      for (int j = 0; j < K - 1; ++j) win[j + 1] = to_f32<BF16>(in[j]);
 #pragma unroll
-      for (int j = 0; j < K; ++j)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) dus[j].v[e] = 0.f;
+      for (int j = 0; j < K; ++j) dus[j] = zero;
       const bool first = t0 == 0 && a.dstate0;
 #pragma unroll
       for (int s = 0; s < S + K - 1; ++s) {
@@ -189,90 +224,65 @@ __global__ __launch_bounds__(NT) void ttt_conv_bwd_k(ConvBackwardArgs a) {
           win[j] = win[j + 1];
           dus[j] = dus[j + 1];
         }
-        win[K - 1] = widen8(in8[s + K - 1]);
-        F8 du = widen8(g8[s]);
+        win[K - 1] = to_f32<BF16>(in[s + K - 1]);
+        f32x4 du = to_f32<BF16>(g[s]);
         if (a.silu) {
-          F8 u = flt.bias;
+          f32x4 u = bias;
 #pragma unroll
-          for (int j = 0; j < K; ++j)
+          for (int j = 0; j < K; ++j) u += w[j] * win[j];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) u.v[e] += flt.w[j].v[e] * win[j].v[e];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float sg = sigmoid(u.v[e]);
-            du.v[e] *= sg * (1.0f + u.v[e] * (1.0f - sg));
+          for (int e = 0; e < 4; ++e) {
+            const float sg = sigmoid(u[e]);
+            du[e] *= sg * (1.0f + u[e] * (1.0f - sg));
           }
         }
         dus[K - 1] = du;
         if (s < S && t0 + s < T) {
+          acc[K] += du;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) acc[K].v[e] += du.v[e];
-#pragma unroll
-          for (int j = 0; j < K; ++j)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) acc[j].v[e] += du.v[e] * win[j].v[e];
+          for (int j = 0; j < K; ++j) acc[j] += du * win[j];
         }
         // dx of token t0 + s - (K-1): its du's are dus[0..K-1]
         const int t = t0 + s - (K - 1);
         if ((s >= K - 1 && t < T) || (first && s < K - 1)) {
-          F8 dx;
+          f32x4 dx = zero;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            dx.v[e] = 0.f;
-#pragma unroll
-            for (int j = 0; j < K; ++j) dx.v[e] += flt.w[K - 1 - j].v[e] * dus[j].v[e];
-          }
-          if (a.dstate && t >= T - (K - 1)) {   // also an input of the final state
-            const F8 g = load8<BF16>(a.dstate, (unit * (K - 1) + (t - (T - (K - 1)))) * d + f);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) dx.v[e] += g.v[e];
-          }
-          if (t >= 0) store8<BF16>(a.dx, (unit * T + t) * d + f, dx);
-          else store8<BF16>(a.dstate0, (unit * (K - 1) + (t + K - 1)) * d + f, dx);
+          for (int j = 0; j < K; ++j) dx += w[K - 1 - j] * dus[j];
+          if (a.dstate && t >= T - (K - 1))   // also an input of the final state
+            dx += to_f32<BF16>(
+                load4_raw<BF16>(a.dstate, (unit * (K - 1) + (t - (T - (K - 1)))) * d + f));
+          if (t >= 0) store4<BF16>(a.dx, (unit * T + t) * d + f, dx);
+          else store4<BF16>(a.dstate0, (unit * (K - 1) + (t + K - 1)) * d + f, dx);
         }
       }
     }
+#pragma unroll
+    for (int j = 0; j <= K; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) red[j][e][threadIdx.x] = acc[j][e];
   }
+  __syncthreads();
   float* out = a.partial +
                ((static_cast<size_t>(b) * a.chunks + chunk) * a.H + h) * (K + 1) * d;
-#pragma unroll
-  for (int j = 0; j <= K; ++j) {
-    __syncthreads();
-    if (row < rows) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) red[threadIdx.x][e] = acc[j].v[e];
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < d; i += NT) {
-      float s = 0.f;
-      for (int r = 0; r < rows; ++r) s += red[r * lanes + i / 8][i % 8];
-      out[static_cast<size_t>(j) * d + i] = s;
-    }
+  for (int i = threadIdx.x; i < (K + 1) * d; i += NT) {
+    const int j = i / d, in = i - j * d;
+    const float* p = &red[j][in & 3][in >> 2];
+    float s = 0.f;
+    for (int r = 0; r < rows; ++r) s += p[r * lanes];
+    out[i] = s;
   }
 }
 
-// dw, dbias: the partials of every (batch, chunk) in order; 16 columns per
-// workgroup, 16 threads a column.
+// dw, dbias: the partials of every (batch, chunk) in order.
 template <int K>
 __global__ __launch_bounds__(NT) void ttt_conv_bwd_sum_k(ConvBackwardArgs a) {
-  __shared__ float part[16][17];
-  const int col = threadIdx.x & 15, slot = threadIdx.x >> 4;
   const size_t n = static_cast<size_t>(a.H) * (K + 1) * a.d;
-  const size_t i = 16 * static_cast<size_t>(blockIdx.x) + col;
-  const int64_t parts = static_cast<int64_t>(a.B) * a.chunks;
-  float s = 0.f;
-  if (i < n)
-    for (int64_t p = slot; p < parts; p += 16) s += a.partial[p * n + i];
-  part[slot][col] = s;
-  __syncthreads();
-  if (slot == 0 && i < n) {
-#pragma unroll
-    for (int k = 1; k < 16; ++k) s += part[k][col];
+  column_sums(a.partial, n, static_cast<int64_t>(a.B) * a.chunks, [&](size_t i, float s) {
     const size_t h = i / (static_cast<size_t>(K + 1) * a.d);
     const int in = static_cast<int>(i - h * (K + 1) * a.d);
     if (in < K * a.d) a.dw[h * K * a.d + in] = s;
     else a.dbias[h * a.d + (in - K * a.d)] = s;
-  }
+  });
 }
 
 template <bool BF16, int K>

@@ -5,21 +5,32 @@
 // and its outputs: q, k, v bf16 in [B, H, T, 64] and eta = eta_base /
 // (1 + exp(-(y + b_eta))) fp32.
 //
-// Tiling: 256 x 128 outputs per workgroup, 8 waves of 64 x 64.  D is walked in
-// steps of 128 bytes through three LDS buffers that global_load_lds fills two
-// steps ahead; the 16-byte chunk q of row r sits at chunk q ^ (r % 8).  One
+// Tiling: BM x BN outputs per workgroup, 64 columns (one head, or gates) and
+// BM / WM rows per wave.  D is walked in steps of 128 bytes through two LDS
+// buffers, the next step's copies (global_load_lds) on their way while one is
+// worked on; the 16-byte chunk q of row r sits at chunk q ^ (r % 8).  One
 // 16x16x128 product takes chunks g and g + 4 of its rows (the same for both
 // operands, so the contraction's order does not matter).  D is a multiple of
 // 64: an odd last half step fetches its first half twice and multiplies the
 // second copy by zero.
 //
-// Precision.  The 8-bit matrix product adds its 128 exact products with fewer
-// bits than fp32 (measured: 2e-5 of a sum's typical size), far below the bf16
-// rounding of q, k, v but not below that of an fp32 gate: the waves of the
-// gate columns widen their operands to bf16 (exact) and use the 16x16x32 bf16
-// product, which sums in fp32.  They are 1 column block in 49 at H = 32.
+// The same columns come a second way, f8_block: 64 x 32 outputs per workgroup,
+// each wave a share of D read from memory straight into fragments, the waves'
+// sums joined through LDS.  It makes the gates (below), and all columns where
+// few rows (a token per stream) would leave most compute units without a tile
+// and make every one wait for D / 128 round trips.
+//
+// Precision.  The 8-bit matrix product adds its exact products with fewer bits
+// than fp32 (measured: 1.4e-5 of a sum's typical size, in the 128- and the
+// 32-deep form alike), far below the bf16 rounding of q, k, v but not below
+// that of an fp32 gate: gates are summed by 16x16x32 bf16 products (widening
+// e4m3 to bf16 is exact), whose sums are fp32.  They have workgroups of their
+// own, the launch's first: 1 column in 193, and a branch for them inside the
+// tile's loop cost its schedule (527 -> XXX us at B4 T8192 D2048 H32).
 //
 // Tile order over the 8 XCDs as in ttt_input.hip.
+#include <type_traits>
+
 #include "ttt_block.hpp"
 #include "ttt_device.hpp"
 
@@ -30,12 +41,7 @@ namespace {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
-constexpr int BM = 256, BN = 128, BK = 128, NT = 512, HD = 64, XCDS = 8, GM = 4;
-
-struct F8Lds {
-  uint8_t a[3][BM][BK];
-  uint8_t b[3][BN][BK];
-};
+constexpr int BK = 128, HD = 64, XCDS = 8, GM = 4;
 
 __device__ __forceinline__ float sigmoid(float y) { return 1.0f / (1.0f + expf(-y)); }
 
@@ -67,12 +73,38 @@ __device__ __forceinline__ u32x4 widen(uint32_t lo, uint32_t hi) {
   return r;
 }
 
-__global__ __launch_bounds__(NT) void ttt_input_f8_k(InputF8Args a) {
-  __shared__ F8Lds L;
-  const int M = a.B * a.T, N = 3 * a.H * HD + a.H, D = a.D;
+// The product of two steps of 128 bytes in bf16.
+__device__ __forceinline__ f32x4 mfma_widened(u32x4 a0, u32x4 a1, u32x4 b0, u32x4 b1, f32x4 c) {
+  c = mfma32(widen(a0.x, a0.y), widen(b0.x, b0.y), c);
+  c = mfma32(widen(a0.z, a0.w), widen(b0.z, b0.w), c);
+  c = mfma32(widen(a1.x, a1.y), widen(b1.x, b1.y), c);
+  return mfma32(widen(a1.z, a1.w), widen(b1.z, b1.w), c);
+}
+
+__device__ __forceinline__ uint16_t* head_out(const InputF8Args& a, int col, int* h) {
+  const int which = col / (a.H * HD);
+  *h = (col / HD) % a.H;
+  return which == 0 ? static_cast<uint16_t*>(a.q)
+                    : which == 1 ? static_cast<uint16_t*>(a.k) : static_cast<uint16_t*>(a.v);
+}
+
+// WM x WN waves of 16 MI rows x 64 columns.
+template <int WM, int WN, int MI>
+struct F8Tile {
+  static constexpr int BM = WM * MI * 16, BN = WN * 64, NT = WM * WN * 64;
+  static constexpr int COPIES_A = BM / 8 / (WM * WN), COPIES_B = BN / 8 / (WM * WN);
+  uint8_t a[2][BM][BK];
+  uint8_t b[2][BN][BK];
+};
+
+template <int WM, int WN, int MI>
+__device__ __forceinline__ void f8_tile(const InputF8Args& a, F8Tile<WM, WN, MI>& L, int id) {
+  using Tile = F8Tile<WM, WN, MI>;
+  constexpr int BM = Tile::BM, BN = Tile::BN, CA = Tile::COPIES_A, CB = Tile::COPIES_B;
+  const int M = a.B * a.T, N = 3 * a.H * HD, D = a.D;   // without the gates
   const int ntm = (M + BM - 1) / BM, ntn = (N + BN - 1) / BN, nt = ntm * ntn;
   const int per = (nt + XCDS - 1) / XCDS;
-  const int tile = (blockIdx.x % XCDS) * per + blockIdx.x / XCDS;
+  const int tile = (id % XCDS) * per + id / XCDS;
   if (tile >= nt) return;
   const int grp = tile / (GM * ntn), within = tile % (GM * ntn);
   const int gsize = min(GM, ntm - grp * GM);
@@ -80,127 +112,158 @@ __global__ __launch_bounds__(NT) void ttt_input_f8_k(InputF8Args a) {
 
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int g = lane >> 4, c = lane & 15;
-  const int wm = wave >> 1, wn = wave & 1;
+  const int wm = wave / WN, wn = wave % WN;
 
-  // copies: as in ttt_input.hip, 8 rows of 128 bytes per wave instruction;
-  // rows past M and N are clamped (valid memory, results unused)
+  // copies: 8 rows of 128 bytes per wave instruction, lane l landing at byte
+  // 16 l; rows past M and N are clamped (valid memory, results unused)
   const int cr = lane >> 3, cq = lane & 7;
-  const uint8_t* xg = static_cast<const uint8_t*>(a.x);
-  const uint8_t* wg = static_cast<const uint8_t*>(a.w);
-  const uint8_t* pa[4];
-  const uint8_t* pb[2];
-  // chunk fetched by this lane (rows of a block: r % 8 = cr), and the one
-  // that takes its place in a half step (chunks 4-7 lie past the row's end)
+  const uint8_t* xg = static_cast<const uint8_t*>(a.x) + static_cast<size_t>(m0) * D;
+  const uint8_t* wg = static_cast<const uint8_t*>(a.w) + static_cast<size_t>(n0) * D;
+  uint32_t oa[CA], ob[CB];   // within the tile's rows
+#pragma unroll
+  for (int j = 0; j < CA; ++j)
+    oa[j] = static_cast<uint32_t>(min(8 * (wave + WM * WN * j) + cr, M - 1 - m0)) * D;
+#pragma unroll
+  for (int j = 0; j < CB; ++j)
+    ob[j] = static_cast<uint32_t>(min(8 * (wave + WM * WN * j) + cr, N - 1 - n0)) * D;
+  // the chunk that belongs in this lane's slot (rows of a block: r % 8 = cr),
+  // and the one fetched in its place in a half step (chunks 4-7 lie past the row's end)
   const int full = 16 * (cq ^ cr), half = 16 * ((cq ^ cr) & 3);
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    pa[j] = xg + static_cast<size_t>(min(m0 + 8 * (wave + 8 * j) + cr, M - 1)) * D;
-#pragma unroll
-  for (int j = 0; j < 2; ++j)
-    pb[j] = wg + static_cast<size_t>(min(n0 + 8 * (wave + 8 * j) + cr, N - 1)) * D;
   const int steps = (D + BK - 1) / BK;
   const bool odd = D % BK != 0;
-  auto issue = [&](int buf, int step) {
-    const int s = min(step, steps - 1);   // past the end: the last step again
-    const int at = s * BK + (odd && s == steps - 1 ? half : full);
+  auto issue = [&](int s) {
+    const int buf = s & 1;
+    const uint32_t at = s * BK + (odd && s == steps - 1 ? half : full);
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      __builtin_amdgcn_global_load_lds(pa[j] + at, (TTT_LDS void*)&L.a[buf][8 * (wave + 8 * j)][0],
-                                       16, 0, 0);
+    for (int j = 0; j < CA; ++j)
+      __builtin_amdgcn_global_load_lds(
+          xg + (oa[j] + at), (TTT_LDS void*)&L.a[buf][8 * (wave + WM * WN * j)][0], 16, 0, 0);
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-      __builtin_amdgcn_global_load_lds(pb[j] + at, (TTT_LDS void*)&L.b[buf][8 * (wave + 8 * j)][0],
-                                       16, 0, 0);
+    for (int j = 0; j < CB; ++j)
+      __builtin_amdgcn_global_load_lds(
+          wg + (ob[j] + at), (TTT_LDS void*)&L.b[buf][8 * (wave + WM * WN * j)][0], 16, 0, 0);
   };
 
-  f32x4 acc[4][4];
+  f32x4 acc[MI][4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < MI; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  const int QKV = 3 * a.H * HD;
   const int nb0 = n0 + 64 * wn;
-  const bool gate = nb0 >= QKV;             // of the wave; its 64 columns are one kind
   const u32x4 zero = {0, 0, 0, 0};
-  auto compute = [&](int buf, bool whole) {
-    u32x4 a0[4], a1[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint8_t* row = L.a[buf][64 * wm + 16 * i + c];
-      a0[i] = chunk(row, g, c);
-      a1[i] = whole ? chunk(row, g + 4, c) : zero;
-    }
+  u32x4 a0[MI], a1[MI], b0[4], b1[4];
+  auto read = [&](int buf, auto whole) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const uint8_t* row = L.b[buf][64 * wn + 16 * j + c];
-      const u32x4 b0 = chunk(row, g, c);
-      const u32x4 b1 = whole ? chunk(row, g + 4, c) : zero;
-      if (!gate) {
+      b0[j] = chunk(row, g, c);
+      b1[j] = whole ? chunk(row, g + 4, c) : zero;
+    }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[i][j] = mfma_f8(a0[i], a1[i], b0, b1, acc[i][j]);
-      } else if (nb0 + 16 * j < N) {
-        const u32x4 w0 = widen(b0.x, b0.y), w1 = widen(b0.z, b0.w);
-        const u32x4 w2 = widen(b1.x, b1.y), w3 = widen(b1.z, b1.w);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          acc[i][j] = mfma32(widen(a0[i].x, a0[i].y), w0, acc[i][j]);
-          acc[i][j] = mfma32(widen(a0[i].z, a0[i].w), w1, acc[i][j]);
-          acc[i][j] = mfma32(widen(a1[i].x, a1[i].y), w2, acc[i][j]);
-          acc[i][j] = mfma32(widen(a1[i].z, a1[i].w), w3, acc[i][j]);
-        }
-      }
+    for (int i = 0; i < MI; ++i) {
+      const uint8_t* row = L.a[buf][16 * MI * wm + 16 * i + c];
+      a0[i] = chunk(row, g, c);
+      a1[i] = whole ? chunk(row, g + 4, c) : zero;
     }
   };
-
-  issue(0, 0);
-  issue(1, 1);
-  asm volatile("s_waitcnt vmcnt(6)" ::: "memory");
-  lds_barrier_copies_in_flight();
-  int cur = 0;
-  for (int s = 0; s < steps; ++s) {
-    compute(cur, !(odd && s == steps - 1));
-    issue(cur == 0 ? 2 : cur - 1, s + 2);   // buffer (s + 2) % 3
-    asm volatile("s_waitcnt vmcnt(6)" ::: "memory");
+  auto multiply = [&] {
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] = mfma_f8(a0[i], a1[i], b0[j], b1[j], acc[i][j]);
+  };
+  auto landed = [] { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); };
+  // a barrier that products do not cross either
+  auto meet = [] {
+    __builtin_amdgcn_sched_barrier(0);
     lds_barrier_copies_in_flight();
-    cur = cur == 2 ? 0 : cur + 1;
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  if constexpr (WM * WN == 8) {
+    // Two waves per SIMD, waves w and w + 4, half a step apart: while one
+    // group reads its fragments, the other's products run.  With phases
+    // between barriers, the first group reads step s in phase 2 s and
+    // multiplies in 2 s + 1, the second a phase later; step s + 2 may replace
+    // s in its buffer from phase 2 s + 2 on, and has to have landed by the
+    // end of 2 s + 3.
+    const bool second = wave >= 4;
+    issue(0);
+    if (steps > 1) {
+      issue(1);
+      asm volatile("s_waitcnt vmcnt(%0)" ::"n"(CA + CB) : "memory");
+    } else {
+      landed();
+    }
+    meet();
+    auto step = [&](int s, auto whole) {
+      if (!second && s > 0 && s + 1 < steps) issue(s + 1);
+      read(s & 1, whole);
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      if (second) landed();
+      meet();
+      if (second && s + 2 < steps) issue(s + 2);
+      __builtin_amdgcn_s_setprio(1);
+      multiply();
+      __builtin_amdgcn_s_setprio(0);
+      __builtin_amdgcn_sched_barrier(0);
+      if (!second) landed();
+      meet();
+    };
+    if (second) meet();
+    const int whole = odd ? steps - 1 : steps;
+    for (int s = 0; s < whole; ++s) step(s, std::true_type{});
+    if (odd) step(whole, std::false_type{});
+    if (!second) meet();
+  } else {
+    // One wave per SIMD and two workgroups per compute unit: the other
+    // workgroup's products run beside this one's reads.
+    auto step = [&](int s, auto whole) {
+      if (s + 1 < steps) issue(s + 1);
+      read(s & 1, whole);
+      multiply();
+      landed();
+      lds_barrier_copies_in_flight();
+    };
+    issue(0);
+    landed();
+    lds_barrier_copies_in_flight();
+    const int whole = odd ? steps - 1 : steps;
+    for (int s = 0; s < whole; ++s) step(s, std::true_type{});
+    if (odd) step(whole, std::false_type{});
   }
-  // the last copies (repeats of the last step) land before the LDS is reused
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  lds_barrier_copies_in_flight();
 
-  // epilogue: accumulator (i, j) holds row m0 + 64 wm + 16 i + 4 g + r, column nb0 + 16 j + c
+  // epilogue: accumulator (i, j) holds row m0 + 16 (MI wm + i) + 4 g + r, column nb0 + 16 j + c
   const int T = a.T, H = a.H;
   float sw[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) sw[j] = a.w_scale[min(nb0 + 16 * j + c, N - 1)];
-  float sx[4][4];
+  if (nb0 >= N) return;
+  // 64 output rows of 128 bytes at a time, staged through the wave's own 8 KB of LDS
+  static_assert(sizeof(Tile) >= static_cast<size_t>(WM) * WN * 8192, "staging fits");
+  uint16_t (*W)[64] = reinterpret_cast<uint16_t (*)[64]>(&L.a[0][0][0]) + 64 * wave;
+  int h;
+  uint16_t* out = head_out(a, nb0, &h);
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-      sx[i][r] = a.x_scale[min(m0 + 64 * wm + 16 * i + 4 * g + r, M - 1)];
-  if (!gate) {
-    // 64 output rows of 128 bytes, staged through the wave's own 8 KB of LDS
-    uint16_t (*W)[64] = reinterpret_cast<uint16_t (*)[64]>(&L.a[0][0][0]) + 64 * wave;
+  for (int part = 0; part < MI / 4; ++part) {
+    const int mp = m0 + 16 * (MI * wm + 4 * part);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int r = 0; r < 4; ++r) {
+        const int row = 16 * i + 4 * g + r;
+        const float sx = a.x_scale[min(mp + row, M - 1)];
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          W[16 * i + 4 * g + r][(16 * j + c) ^ (((4 * g + r) & 7) << 3)] = static_cast<uint16_t>(
-              pack_bf16(acc[i][j][r] * (sx[i][r] * sw[j]), 0.f) & 0xffffu);
+        for (int j = 0; j < 4; ++j)
+          W[row][(16 * j + c) ^ ((row & 7) << 3)] = static_cast<uint16_t>(
+              pack_bf16(acc[4 * part + i][j][r] * (sx * sw[j]), 0.f) & 0xffffu);
+      }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the wave's own rows, in order
-    const int which = nb0 / (H * HD), h = (nb0 / HD) % H;
-    uint16_t* out = which == 0 ? static_cast<uint16_t*>(a.q)
-                               : which == 1 ? static_cast<uint16_t*>(a.k)
-                                            : static_cast<uint16_t*>(a.v);
     const int col = 8 * (lane & 7);
 #pragma unroll
     for (int pass = 0; pass < 8; ++pass) {
       const int row = (lane >> 3) + 8 * pass;
-      const int m = m0 + 64 * wm + row;
+      const int m = mp + row;
       const u32x4 val = *reinterpret_cast<const u32x4*>(&W[row][col ^ ((row & 7) << 3)]);
       if (m < M) {
         const int b = m / T, t = m - b * T;
@@ -208,33 +271,150 @@ __global__ __launch_bounds__(NT) void ttt_input_f8_k(InputF8Args a) {
             val;
       }
     }
-  } else {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // read before the next part's writes
+  }
+}
+
+// 64 x 32 outputs, wave w of W taking steps w, w + W, ... of D.  GATE: the
+// columns are gates (n0 counts from the first).
+constexpr int FM = 64, FN = 32;
+
+template <int W>
+using F8Part = f32x4[W][8][64];
+
+template <int W, bool GATE>
+__device__ __forceinline__ void f8_block(const InputF8Args& a, F8Part<W>& part, int m0, int n0) {
+  const int M = a.B * a.T, QKV = 3 * a.H * HD, N = GATE ? a.H : QKV, D = a.D;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, c = lane & 15;
+  const int first = GATE ? QKV : 0;
+  const uint8_t* pa[4];
+  const uint8_t* pb[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < 4; ++i)
+    pa[i] = static_cast<const uint8_t*>(a.x) +
+            static_cast<size_t>(min(m0 + 16 * i + c, M - 1)) * D + 16 * g;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int m = m0 + 64 * wm + 16 * i + 4 * g + r;
-        if (m >= M) continue;
-        const int b = m / T, t = m - b * T;
+  for (int j = 0; j < 2; ++j)
+    pb[j] = static_cast<const uint8_t*>(a.w) +
+            static_cast<size_t>(first + min(n0 + 16 * j + c, N - 1)) * D + 16 * g;
+  f32x4 acc[4][2];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int h = nb0 + 16 * j + c - QKV;
-          if (h < H)
-            a.eta[(static_cast<size_t>(b) * H + h) * T + t] =
-                a.eta_base * sigmoid(acc[i][j][r] * (sx[i][r] * sw[j]) + a.b_eta[h]);
-        }
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const u32x4 zero = {0, 0, 0, 0};
+  for (int k = BK * wave; k < D; k += BK * W) {
+    const bool whole = k + BK <= D;   // else the last 64 bytes
+    u32x4 a0[4], a1[4], b0[2], b1[2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      a0[i] = *reinterpret_cast<const u32x4*>(pa[i] + k);
+      a1[i] = whole ? *reinterpret_cast<const u32x4*>(pa[i] + k + 64) : zero;
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      b0[j] = *reinterpret_cast<const u32x4*>(pb[j] + k);
+      b1[j] = whole ? *reinterpret_cast<const u32x4*>(pb[j] + k + 64) : zero;
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (!GATE) acc[i][j] = mfma_f8(a0[i], a1[i], b0[j], b1[j], acc[i][j]);
+        else acc[i][j] = mfma_widened(a0[i], a1[i], b0[j], b1[j], acc[i][j]);
       }
   }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) part[wave][2 * i + j][lane] = acc[i][j];
+  __syncthreads();
+  // wave w joins blocks w, w + W, ...: row block i / 2, column block i % 2
+  for (int i = wave; i < 8; i += W) {
+    f32x4 sum = part[0][i][lane];
+#pragma unroll
+    for (int k = 1; k < W; ++k) sum += part[k][i][lane];
+    const int col = n0 + 16 * (i & 1) + c;
+    if (col >= N) continue;
+    const float sw = a.w_scale[first + col];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int m = m0 + 16 * (i >> 1) + 4 * g + r;
+      if (m >= M) break;
+      const int b = m / a.T, t = m - b * a.T;
+      const float y = sum[r] * (a.x_scale[m] * sw);
+      if constexpr (GATE) {
+        a.eta[(static_cast<size_t>(b) * a.H + col) * a.T + t] =
+            a.eta_base * sigmoid(y + a.b_eta[col]);
+      } else {
+        int h;
+        uint16_t* out = head_out(a, col, &h);
+        out[((static_cast<size_t>(b) * a.H + h) * a.T + t) * HD + col % HD] =
+            static_cast<uint16_t>(pack_bf16(y, 0.f) & 0xffffu);
+      }
+    }
+  }
+}
+
+// Workgroups of the gates of `rows` rows and H heads.
+__host__ __device__ inline int gate_blocks(int rows, int H) {
+  return ((rows + FM - 1) / FM) * ((H + FN - 1) / FN);
+}
+
+// The bodies are device functions: the host pass leaves a kernel template that
+// holds the 16-byte global_load_lds without its launch stub.
+template <int WM, int WN, int MI>
+__global__ __launch_bounds__(WM * WN * 64) void ttt_input_f8_k(InputF8Args a) {
+  constexpr int W = WM * WN;
+  constexpr size_t bytes = sizeof(F8Tile<WM, WN, MI>) > sizeof(F8Part<W>)
+                               ? sizeof(F8Tile<WM, WN, MI>) : sizeof(F8Part<W>);
+  __shared__ alignas(16) char smem[bytes];
+  const int gates = (gate_blocks(a.B * a.T, a.H) + XCDS - 1) / XCDS * XCDS;
+  const int id = blockIdx.x;
+  if (id >= gates) {
+    f8_tile<WM, WN, MI>(a, *reinterpret_cast<F8Tile<WM, WN, MI>*>(smem), id - gates);
+  } else if (id < gate_blocks(a.B * a.T, a.H)) {
+    const int cols = (a.H + FN - 1) / FN;
+    f8_block<W, true>(a, *reinterpret_cast<F8Part<W>*>(smem), id / cols * FM, id % cols * FN);
+  }
+}
+
+__global__ __launch_bounds__(512) void ttt_input_f8_few_k(InputF8Args a) {
+  __shared__ F8Part<8> part;
+  const int gates = gate_blocks(a.B * a.T, a.H), id = blockIdx.x;
+  if (id < gates) {
+    const int cols = (a.H + FN - 1) / FN;
+    f8_block<8, true>(a, part, id / cols * FM, id % cols * FN);
+  } else {
+    const int cols = 3 * a.H * HD / FN;
+    f8_block<8, false>(a, part, (id - gates) / cols * FM, (id - gates) % cols * FN);
+  }
+}
+
+template <int WM, int WN, int MI>
+hipError_t tile_launch(const InputF8Args& a, hipStream_t stream) {
+  using Tile = F8Tile<WM, WN, MI>;
+  const int64_t M = static_cast<int64_t>(a.B) * a.T, N = 3 * static_cast<int64_t>(a.H) * HD;
+  const int64_t nt = ((M + Tile::BM - 1) / Tile::BM) * ((N + Tile::BN - 1) / Tile::BN);
+  const int64_t gates = gate_blocks(static_cast<int>(M), a.H);
+  const int64_t blocks = (gates + XCDS - 1) / XCDS * XCDS + (nt + XCDS - 1) / XCDS * XCDS;
+  hipLaunchKernelGGL((ttt_input_f8_k<WM, WN, MI>), dim3(static_cast<uint32_t>(blocks)),
+                     dim3(Tile::NT), 0, stream, a);
+  return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_input_f8(const InputF8Args& a, hipStream_t stream) {
-  const int64_t M = static_cast<int64_t>(a.B) * a.T, N = 3 * static_cast<int64_t>(a.H) * HD + a.H;
-  const int64_t nt = ((M + BM - 1) / BM) * ((N + BN - 1) / BN);
-  hipLaunchKernelGGL(ttt_input_f8_k, dim3(static_cast<uint32_t>((nt + XCDS - 1) / XCDS * XCDS)),
-                     dim3(NT), 0, stream, a);
-  return hipGetLastError();
+  const int64_t M = static_cast<int64_t>(a.B) * a.T, N = 3 * static_cast<int64_t>(a.H) * HD;
+  if (M <= 128) {
+    const int64_t blocks = gate_blocks(static_cast<int>(M), a.H) + ((M + FM - 1) / FM) * (N / FN);
+    hipLaunchKernelGGL(ttt_input_f8_few_k, dim3(static_cast<uint32_t>(blocks)), dim3(512), 0,
+                       stream, a);
+    return hipGetLastError();
+  }
+  if (((M + 255) / 256) * ((N + 255) / 256) >= 256) return tile_launch<2, 4, 8>(a, stream);
+  return tile_launch<2, 2, 4>(a, stream);
 }
 
 }  // namespace tttk

@@ -212,22 +212,9 @@ __global__ __launch_bounds__(NT) void ttt_norm_bwd_k(NormBackwardArgs a) {
   }
 }
 
-// dweight[f] = sum over the groups' partial rows: 16 columns per workgroup,
-// 16 threads a column, joined in order.
+// dweight[f]: the groups' partial rows in order.
 __global__ __launch_bounds__(NT) void ttt_norm_bwd_sum_k(NormBackwardArgs a) {
-  __shared__ float part[16][17];
-  const int col = threadIdx.x & 15, slot = threadIdx.x >> 4;
-  const int f = 16 * blockIdx.x + col;
-  float s = 0.f;
-  if (f < a.width)
-    for (int g = slot; g < a.groups; g += 16) s += a.partial[static_cast<size_t>(g) * a.width + f];
-  part[slot][col] = s;
-  __syncthreads();
-  if (slot == 0 && f < a.width) {
-#pragma unroll
-    for (int k = 1; k < 16; ++k) s += part[k][col];
-    a.dweight[f] = s;
-  }
+  column_sums(a.partial, a.width, a.groups, [&](size_t f, float s) { a.dweight[f] = s; });
 }
 
 // Widths by the number of 8-value steps that their row takes.

@@ -44,7 +44,10 @@ def check(got, want, D):
 
 @pytest.mark.parametrize("B,T,D,H", [(1, 1, 64, 1), (2, 100, 128, 2), (3, 257, 192, 3),
                                      (1, 300, 768, 12), (2, 33, 64, 5), (61, 1, 768, 12),
-                                     (1, 513, 2048, 2), (4, 300, 320, 40)],
+                                     (1, 513, 2048, 2), (4, 300, 320, 40),
+                                     # enough 256 x 256 tiles for the larger workgroup, with
+                                     # one step of D, a half step behind one, and several
+                                     (1, 2300, 64, 40), (3, 767, 192, 40), (2, 1100, 512, 41)],
                          ids=lambda v: str(v))
 def test_matches_the_oracle(B, T, D, H):
     x, xs, w, ws, be = make(B, T, D, H)
