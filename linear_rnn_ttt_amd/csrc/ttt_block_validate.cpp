@@ -112,14 +112,13 @@ struct Segments {
   int32_t tiles, segs, seg_tiles;
 };
 
-// Time segments of one unit: enough workgroups to fill the 256 compute units
-// several times over while a unit's tiles allow it.
-Segments ssm_segments(const ttt_params* p, uint64_t want) {
+// Time segments of one unit: as many as fill the card once.
+Segments ssm_segments(const ttt_params* p, uint64_t workgroups) {
   const uint64_t units = static_cast<uint64_t>(p->B) * p->H;
   const int32_t tile = ssm_tile(p);
   Segments s;
   s.tiles = (p->T + tile - 1) / tile;
-  uint64_t segs = (want + units - 1) / units;
+  uint64_t segs = workgroups / units;
   if (segs > static_cast<uint64_t>(s.tiles)) segs = s.tiles;
   if (segs < 1) segs = 1;
   s.seg_tiles = static_cast<int32_t>((s.tiles + segs - 1) / segs);
@@ -127,7 +126,14 @@ Segments ssm_segments(const ttt_params* p, uint64_t want) {
   return s;
 }
 
-constexpr uint64_t kForwardWorkgroups = 1024, kBackwardWorkgroups = 512;
+// Workgroups that 256 compute units hold at once (by their LDS and registers).
+uint64_t scan_workgroups(const ttt_params* p, int32_t n) {
+  if (n == 128) return 256 * 2;
+  return 256 * (p->io_dtype == TTT_BF16 || n == 32 ? 4 : 3);
+}
+uint64_t grad_workgroups(const ttt_params* p, int32_t n) {
+  return 256 * (n == 32 || (n == 64 && p->io_dtype == TTT_BF16) ? 2 : 1);
+}
 
 ttt_status check_ssm(const ttt_params* p, int32_t groups, int32_t n, uint64_t* units,
                      uint64_t* es) {
@@ -145,7 +151,7 @@ struct ForwardLayout {
   uint64_t fade, total;
 };
 ForwardLayout ssm_layout(const ttt_params* p, int32_t n) {
-  const Segments s = ssm_segments(p, kForwardWorkgroups);
+  const Segments s = ssm_segments(p, scan_workgroups(p, n));
   const uint64_t units = static_cast<uint64_t>(p->B) * p->H;
   ForwardLayout ly{0, 0};
   if (s.segs > 1) {
@@ -159,12 +165,12 @@ struct BackwardLayout {
   uint64_t seg, fade, adj, tile, sums, db, dc, total;
 };
 BackwardLayout ssm_backward_layout(const ttt_params* p, int32_t groups, int32_t n) {
-  const Segments s = ssm_segments(p, kBackwardWorkgroups);
+  const Segments s = ssm_segments(p, grad_workgroups(p, n));
   const uint64_t units = static_cast<uint64_t>(p->B) * p->H;
   const uint64_t sb = state_bytes(n);
   BackwardLayout ly;
-  ly.seg = 0;                                                   // [units][segs + 1] states
-  ly.adj = ly.seg + units * (s.segs + 1) * sb;                  // [units][segs] adjoints
+  ly.seg = 0;                                                   // [units][segs] states
+  ly.adj = ly.seg + units * s.segs * sb;                        // [units][segs] adjoints
   ly.tile = ly.adj + units * s.segs * sb;                       // [units][tiles] states
   ly.fade = ly.tile + units * s.tiles * sb;
   ly.sums = ly.fade + up256(units * s.segs * 8);
@@ -419,7 +425,7 @@ ttt_status ssm_forward(const ttt_params* p, int32_t groups, int32_t n, const voi
   fill_ssm(p, groups, n, x, dt, a, b, c, d_skip, state0, out);
   out->y = y;
   out->state_out = state_out;
-  const Segments s = ssm_segments(p, kForwardWorkgroups);
+  const Segments s = ssm_segments(p, scan_workgroups(p, n));
   out->segs = s.segs;
   out->seg_tiles = s.seg_tiles;
   if (s.segs > 1) {
@@ -486,7 +492,7 @@ ttt_status ssm_backward(const ttt_params* p, int32_t groups, int32_t n, const vo
                    span(dstate, sb)}))
     return TTT_ERR_ALIAS;
   fill_ssm(p, groups, n, x, dt, a, b, c, d_skip, state0, &out->f);
-  const Segments s = ssm_segments(p, kBackwardWorkgroups);
+  const Segments s = ssm_segments(p, grad_workgroups(p, n));
   char* base = static_cast<char*>(workspace);
   out->f.segs = s.segs;
   out->f.seg_tiles = s.seg_tiles;

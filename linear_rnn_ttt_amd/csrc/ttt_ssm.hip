@@ -42,49 +42,56 @@ struct StatesLds {
   static constexpr int L = kSsmTile<NI>;
   Plane<NI, L, P> x;
   Plane<NI, L, N> b;
-  Tokens<L> tk;
-  float fade;
+  Tokens<L> tk[2];   // of even and odd tiles
 };
 
 template <int NI, int N>
-__global__ __launch_bounds__(NT) void ttt_ssm_states_k(SsmArgs a) {
+__global__ __launch_bounds__(NT, 2) void ttt_ssm_states_k(SsmArgs a) {
   constexpr int L = kSsmTile<NI>;
   __shared__ alignas(16) StatesLds<NI, N> lds;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, c = lane & 15;
-  const int seg = blockIdx.x % a.segs;
-  const size_t unit = blockIdx.x / a.segs;
-  const int h = static_cast<int>(unit % a.H);
-  const size_t shared = unit / a.H * a.G + h / (a.H / a.G);
-  const int tiles = (a.T + L - 1) / L;
-  const int first = seg * a.seg_tiles, end = min(first + a.seg_tiles, tiles);
+  const Place at(a, blockIdx.x, a.segs - 1);   // nothing follows the last segment
+  const int seg = at.seg, h = at.h;
+  const size_t unit = at.unit, shared = at.shared;
+  const int first = seg * a.seg_tiles, end = first + a.seg_tiles;
   const float ah = a.a[h];
   f32x4 S[N / 16];
 #pragma unroll
   for (int i = 0; i < N / 16; ++i) S[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  Fetch<NI, L, P, NT> fx;
-  Fetch<NI, L, N, NT> fb;
-  float step = 0.f;
-  auto fetch = [&](int tile) {
-    const int t0 = tile * L, valid = min(L, a.T - t0);
-    fx.load(row_ptr<NI>(a.x, unit * a.T + t0, P), valid, tid);
-    fb.load(row_ptr<NI>(a.b, shared * a.T + t0, N), valid, tid);
-    step = lane < valid ? a.dt[unit * a.T + t0 + lane] : 0.f;
+  struct Tile {
+    Fetch<NI, L, P, NT> x;
+    Fetch<NI, L, N, NT> b;
+  } next, after;   // on their way: two tiles
+  auto valid_of = [&](int tile) { return tile < end ? min(L, a.T - tile * L) : 0; };
+  auto fetch = [&](int tile, Tile& to) {
+    const int t0 = tile * L, valid = valid_of(tile);
+    to.x.load(row_ptr<NI>(a.x, unit * a.T + t0, P), valid, tid);
+    to.b.load(row_ptr<NI>(a.b, shared * a.T + t0, N), valid, tid);
   };
+  auto steps_of = [&](int tile) {
+    return load_steps(a.dt + unit * a.T + tile * L, valid_of(tile), lane);
+  };
+  // the decays of a tile are made by one wave while the one before is worked on
   double total = 0.0;
-  fetch(first);
-  for (int tile = first; tile < end; ++tile) {
-    fx.store(lds.x, tid);
-    fb.store(lds.b, tid);
-    if (wave == 0) {
-      const double all = lds.tk.fill(step, ah, lane);
-      total += all;
-      if (lane == 0) lds.fade = exp2_raw(static_cast<float>(all));
-    }
+  fetch(first, next);
+  fetch(first + 1, after);
+  float step = steps_of(first);
+  if (wave == 0) total = lds.tk[first & 1].fill(step, ah, lane);
+  step = steps_of(first + 1);
+  auto work = [&](int tile, Tile& now) {
+    now.x.store(lds.x, tid);
+    now.b.store(lds.b, tid);
     lds_barrier();
-    if (tile + 1 < end) fetch(tile + 1);
-    add_tile<NI, L, N>(
-        S, lds.b, lds.x, lds.fade, [&](int t) { return lds.tk.into_state(t); }, wave, g, c);
+    const Tokens<L>& tk = lds.tk[tile & 1];
+    fetch(tile + 2, now);
+    if (wave == 0 && tile + 1 < end) total += lds.tk[(tile + 1) & 1].fill(step, ah, lane);
+    step = steps_of(tile + 2);
+    add_tile(S, lds.b, 0, lds.x, wave, tk.fade, tk.into, g, c);
     lds_barrier();
+  };
+  for (int tile = first; tile < end; tile += 2) {
+    work(tile, next);
+    if (tile + 1 < end) work(tile + 1, after);
   }
   float* out = a.ws_state + (unit * a.segs + seg) * (N * P);
 #pragma unroll
@@ -98,17 +105,11 @@ __global__ __launch_bounds__(NT) void ttt_ssm_states_k(SsmArgs a) {
 __global__ __launch_bounds__(NT) void ttt_ssm_join_k(SsmArgs a) {
   const int per = a.N * P / 4;   // 16-byte vectors of a state: a multiple of NT
   const uint64_t i = static_cast<uint64_t>(blockIdx.x) * NT + threadIdx.x;
-  const size_t unit = i / per;
-  const size_t at = (i - unit * per) * 4;
-  const size_t size = static_cast<size_t>(a.N) * P;
+  const size_t unit = i / per, at = (i - unit * per) * 4, size = static_cast<size_t>(a.N) * P;
   f32x4 S = {0.f, 0.f, 0.f, 0.f};
   if (a.state0) S = *reinterpret_cast<const f32x4*>(a.state0 + unit * size + at);
-  for (int s = 0; s < a.segs; ++s) {
-    float* p = a.ws_state + (unit * a.segs + s) * size + at;
-    const f32x4 added = *reinterpret_cast<const f32x4*>(p);
-    *reinterpret_cast<f32x4*>(p) = S;
-    S = S * exp2_raw(static_cast<float>(a.ws_fade[unit * a.segs + s])) + added;
-  }
+  join_segments(a.ws_state + unit * a.segs * size + at, size, a.ws_fade + unit * a.segs, a.segs,
+                a.segs - 1, 1, S);
 }
 
 // ---- the scan ---------------------------------------------------------------
@@ -119,21 +120,19 @@ struct ScanLds {
   static constexpr int NM = NI == 1 ? 2 : 3;   // parts of M and of S
   Plane<NI, L, P> x;
   Plane<NI, L, N> b, c;
-  Tokens<L> tk;
-  float fade;
+  Tokens<L> tk[2];          // of even and odd tiles
   Blocks<NM, BLOCKS> m;     // M^T: rows s, columns t
 };
 
 template <int NI, int N>
-__global__ __launch_bounds__(NT) void ttt_ssm_scan_k(SsmArgs a) {
+__global__ __launch_bounds__(NT, 2) void ttt_ssm_scan_k(SsmArgs a) {
   using Lds = ScanLds<NI, N>;
   constexpr int L = Lds::L, TB = Lds::TB, NM = Lds::NM;
   __shared__ alignas(16) Lds lds;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, c = lane & 15;
-  const int seg = blockIdx.x % a.segs;
-  const size_t unit = blockIdx.x / a.segs;
-  const int h = static_cast<int>(unit % a.H);
-  const size_t shared = unit / a.H * a.G + h / (a.H / a.G);
+  const Place at(a, blockIdx.x, a.segs);
+  const int seg = at.seg, h = at.h;
+  const size_t unit = at.unit, shared = at.shared;
   const int tiles = (a.T + L - 1) / L;
   const int first = seg * a.seg_tiles, end = min(first + a.seg_tiles, tiles);
   const float ah = a.a[h], skip = a.d_skip ? a.d_skip[h] : 0.f;
@@ -145,28 +144,35 @@ __global__ __launch_bounds__(NT) void ttt_ssm_scan_k(SsmArgs a) {
 #pragma unroll
     for (int r = 0; r < 4; ++r)
       S[i][r] = from ? from[(16 * i + 4 * g + r) * P + 16 * wave + c] : 0.f;
-  Fetch<NI, L, P, NT> fx;
-  Fetch<NI, L, N, NT> fb, fc;
-  float step = 0.f;
-  auto fetch = [&](int tile) {
-    const int t0 = tile * L, valid = min(L, a.T - t0);
-    fx.load(row_ptr<NI>(a.x, unit * a.T + t0, P), valid, tid);
-    fb.load(row_ptr<NI>(a.b, shared * a.T + t0, N), valid, tid);
-    fc.load(row_ptr<NI>(a.c, shared * a.T + t0, N), valid, tid);
-    step = lane < valid ? a.dt[unit * a.T + t0 + lane] : 0.f;
+  struct Tile {
+    Fetch<NI, L, P, NT> x;
+    Fetch<NI, L, N, NT> b, c;
+  } next;   // on its way
+  auto valid_of = [&](int tile) { return tile < end ? min(L, a.T - tile * L) : 0; };
+  auto fetch = [&](int tile, Tile& to) {
+    const int t0 = tile * L, valid = valid_of(tile);
+    to.x.load(row_ptr<NI>(a.x, unit * a.T + t0, P), valid, tid);
+    to.b.load(row_ptr<NI>(a.b, shared * a.T + t0, N), valid, tid);
+    to.c.load(row_ptr<NI>(a.c, shared * a.T + t0, N), valid, tid);
   };
-  fetch(first);
+  auto steps_of = [&](int tile) {
+    return load_steps(a.dt + unit * a.T + tile * L, valid_of(tile), lane);
+  };
+  fetch(first, next);
+  float step = steps_of(first);
+  if (wave == 0) lds.tk[first & 1].fill(step, ah, lane);
+  step = steps_of(first + 1);
   for (int tile = first; tile < end; ++tile) {
-    const int t0 = tile * L, valid = min(L, a.T - t0);
-    fx.store(lds.x, tid);
-    fb.store(lds.b, tid);
-    fc.store(lds.c, tid);
-    if (wave == 0) {
-      const double all = lds.tk.fill(step, ah, lane);
-      if (lane == 0) lds.fade = exp2_raw(static_cast<float>(all));
-    }
+    const int t0 = tile * L, valid = valid_of(tile);
+    next.x.store(lds.x, tid);
+    next.b.store(lds.b, tid);
+    next.c.store(lds.c, tid);
     lds_barrier();
-    if (tile + 1 < end) fetch(tile + 1);
+    const Tokens<L>& tk = lds.tk[tile & 1];
+    fetch(tile + 1, next);
+    // the decays of the next tile, by the wave that has fewer blocks below
+    if (wave == 3) lds.tk[(tile + 1) & 1].fill(step, ah, lane);
+    step = steps_of(tile + 2);
 
     // M^T block by block: (b_s . c_t), decayed and masked
     for (int i = wave; i < Lds::BLOCKS; i += 4) {
@@ -176,11 +182,10 @@ __global__ __launch_bounds__(NT) void ttt_ssm_scan_k(SsmArgs a) {
 #pragma unroll
       for (int k = 0; k < N / 32; ++k)
         m = mfma_parts(lds.b.rows8(16 * sb, 32 * k, g, c), lds.c.rows8(16 * tb, 32 * k, g, c), m);
-      const int t = 16 * tb + c;
+      m *= tk.fades(tb, 16 * tb + c, 16 * sb + 4 * g) * tk.steps(16 * sb + 4 * g);
+      if (tb == sb) {   // d x_t, as a product too
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int s = 16 * sb + 4 * g + r;
-        m[r] = s <= t ? m[r] * (lds.tk.fade(t, s) * lds.tk.dt[s]) : 0.f;
+        for (int r = 0; r < 4; ++r) m[r] += 4 * g + r == c ? skip : 0.f;
       }
       lds.m.put(i, lane, m);
     }
@@ -197,7 +202,7 @@ __global__ __launch_bounds__(NT) void ttt_ssm_scan_k(SsmArgs a) {
         y[j] = mfma_parts(sp, lds.c.rows(16 * j, 32 * k, g, c), y[j]);
     }
 #pragma unroll
-    for (int j = 0; j < TB; ++j) y[j] *= lds.tk.head[16 * j + c];
+    for (int j = 0; j < TB; ++j) y[j] *= tk.head[16 * j + c];
     lds_barrier();
 
     // and from the tile's own tokens
@@ -216,21 +221,12 @@ __global__ __launch_bounds__(NT) void ttt_ssm_scan_k(SsmArgs a) {
         y[j] = mfma_parts(xs, m, y[j]);
       }
     }
+    const __amdgpu_buffer_rsrc_t out =
+        rows_of(row_ptr<NI>(a.y, unit * a.T + t0, P), valid * P * (NI == 1 ? 2 : 4));
 #pragma unroll
-    for (int j = 0; j < TB; ++j) {
-      const int t = 16 * j + c;
-      if (a.d_skip) y[j] += lds.x.four(t, 16 * wave + 4 * g) * skip;
-      if (t < valid) {
-        const size_t at = (unit * a.T + t0 + t) * P + 16 * wave + 4 * g;
-        if constexpr (NI == 1)
-          *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.y) + at) =
-              u32x2{pack_bf16(y[j][0], y[j][1]), pack_bf16(y[j][2], y[j][3])};
-        else
-          *reinterpret_cast<f32x4*>(static_cast<float*>(a.y) + at) = y[j];
-      }
-    }
-    add_tile<NI, L, N>(
-        S, lds.b, lds.x, lds.fade, [&](int t) { return lds.tk.into_state(t); }, wave, g, c);
+    for (int j = 0; j < TB; ++j)
+      store_row4<NI>(out, 16 * j + c, P, 16 * wave + 4 * g, y[j]);
+    add_tile(S, lds.b, 0, lds.x, wave, tk.fade, tk.into, g, c);
     lds_barrier();
   }
   if (a.state_out && end == tiles) {
@@ -298,7 +294,8 @@ hipError_t scan_launch(const SsmArgs& a, hipStream_t stream) {
   const uint32_t units = static_cast<uint32_t>(a.B) * a.H;
   hipError_t e;
   if (a.segs > 1) {
-    hipLaunchKernelGGL((ttt_ssm_states_k<NI, N>), dim3(units * a.segs), dim3(NT), 0, stream, a);
+    hipLaunchKernelGGL((ttt_ssm_states_k<NI, N>), dim3(units * (a.segs - 1)), dim3(NT), 0, stream,
+                       a);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     hipLaunchKernelGGL(ttt_ssm_join_k, dim3(units * (N * P / 4 / NT)), dim3(NT), 0, stream, a);
     if ((e = hipGetLastError()) != hipSuccess) return e;

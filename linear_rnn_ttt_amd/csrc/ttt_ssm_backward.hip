@@ -25,18 +25,22 @@
 // are fp32.
 //
 // Launches: (1) each segment of tiles walks forward from a state of zero,
-// leaving the state before every tile and what the segment adds; (2) the
-// states in front of the segments; (3) with several segments, what each adds
-// to the adjoint in front of it; (4) the adjoints behind the segments; (5) the
-// gradients, each segment's tiles last to first with A in registers; (6) the
-// sums of da and dd over batch and segments in order; (7) where heads share b
-// and c, their db and dc added in order.
+// leaving the state before every tile and what the segment adds, and the
+// segments behind the first walk backward for what they add to the adjoint in
+// front of them; (2) the states in front of the segments and the adjoints
+// behind them; (3) the gradients, each segment's tiles last to first with A
+// in registers; (4) the sums of da and dd over batch and segments in order;
+// (5) where heads share b and c, their db and dc added in order.
 //
-// In (5) wave w owns features 16 w .. of x (A, dX^T) and rows 16 w .. (and
-// 16 (w + 4) ..) of the state (dB^T, dC^T); A reaches the other waves through
-// LDS.  The matrices W1, W2 and W2^T are shared out by blocks as M in the
-// forward; W2 is made in both orientations (its products are two of eight)
-// rather than transposed.
+// In (3) a workgroup has eight waves: wave w and w + 4 share features 16 w ..
+// of x (of dX^T and A; each has one half of A's rows) and rows 16 w .. (and
+// 16 (w + 4) ..) of the state (of dB^T and dC^T), and each has half of the
+// tile's token blocks, an early and a late one.  A reaches the other waves
+// through LDS, where W1 and W2, shared out by blocks, take its place once it
+// has been read: with bf16 data and N <= 64 two workgroups then fit a compute
+// unit (four waves a SIMD).  W1 and W2 carry dt_s, and W1 d on its diagonal,
+// so that dX, dB and dC come whole from their products; they are written by
+// rows and read by rows or, transposed, by columns.
 #include "ttt_block.hpp"
 #include "ttt_block_io.hpp"
 #include "ttt_ssm_tile.hpp"
@@ -44,7 +48,7 @@
 namespace tttk {
 namespace {
 
-constexpr int NT = SSM_NT, P = SSM_P;
+constexpr int NT = SSM_NT, P = SSM_P, GT = 512;   // GT: threads of a gradient workgroup
 
 // ---- one walk over a segment: the states before its tiles, or its adjoint ---
 
@@ -53,26 +57,22 @@ struct WalkLds {
   static constexpr int L = kSsmTile<NI>;
   Plane<NI, L, P> x;
   Plane<NI, L, N> b;
-  Tokens<L> tk;
-  float fade;
+  Tokens<L> tk[2];   // of even and odd tiles
 };
 
 // ADJ false: S over x and b, first tile to last.  ADJ true: A over dy and c,
 // last to first, for the segments behind the first.
 template <int NI, int N, bool ADJ>
-__global__ __launch_bounds__(NT) void ttt_ssm_bwd_walk_k(SsmBackwardArgs a) {
+__device__ __forceinline__ void walk(const SsmBackwardArgs& a, WalkLds<NI, N>& lds, uint32_t id) {
   constexpr int L = kSsmTile<NI>;
-  __shared__ alignas(16) WalkLds<NI, N> lds;
   const SsmArgs& f = a.f;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, c = lane & 15;
-  const int count = ADJ ? f.segs - 1 : f.segs;
-  const int seg = blockIdx.x % count + (ADJ ? 1 : 0);
-  const size_t unit = blockIdx.x / count;
-  const int h = static_cast<int>(unit % f.H);
-  const size_t shared = unit / f.H * f.G + h / (f.H / f.G);
+  const Place at(f, id, ADJ ? f.segs - 1 : f.segs);
+  const int seg = at.seg + (ADJ ? 1 : 0);
+  const size_t unit = at.unit, shared = at.shared;
   const int tiles = (f.T + L - 1) / L;
-  const int first = seg * f.seg_tiles, end = min(first + f.seg_tiles, tiles);
-  const float ah = f.a[h];
+  const int first = seg * f.seg_tiles, end = min(first + f.seg_tiles, tiles), n = end - first;
+  const float ah = f.a[at.h];
   const void* rows = ADJ ? a.dy : f.x;
   const void* cols = ADJ ? f.c : f.b;
   f32x4 S[N / 16];
@@ -86,65 +86,63 @@ __global__ __launch_bounds__(NT) void ttt_ssm_bwd_walk_k(SsmBackwardArgs a) {
   };
   Fetch<NI, L, P, NT> fx;
   Fetch<NI, L, N, NT> fb;
-  float step = 0.f;
-  auto fetch = [&](int tile) {
-    const int t0 = tile * L, valid = min(L, f.T - t0);
+  auto tile_of = [&](int i) { return ADJ ? end - 1 - i : first + i; };
+  auto valid_of = [&](int i) { return i < n ? min(L, f.T - tile_of(i) * L) : 0; };
+  auto fetch = [&](int i) {
+    const int t0 = tile_of(i) * L, valid = valid_of(i);
     fx.load(row_ptr<NI>(rows, unit * f.T + t0, P), valid, tid);
     fb.load(row_ptr<NI>(cols, shared * f.T + t0, N), valid, tid);
-    step = lane < valid ? f.dt[unit * f.T + t0 + lane] : 0.f;
+  };
+  auto steps_of = [&](int i) {
+    return load_steps(f.dt + unit * f.T + tile_of(i) * L, valid_of(i), lane);
   };
   double total = 0.0;
-  fetch(ADJ ? end - 1 : first);
-  for (int i = 0; i < end - first; ++i) {
-    const int tile = ADJ ? end - 1 - i : first + i;
+  float step = steps_of(0);
+  fetch(0);
+  if (wave == 0) total = lds.tk[0].fill(step, ah, lane);
+  step = steps_of(1);
+  for (int i = 0; i < n; ++i) {
     fx.store(lds.x, tid);
     fb.store(lds.b, tid);
-    if (wave == 0) {
-      const double all = lds.tk.fill(step, ah, lane);
-      total += all;
-      if (lane == 0) lds.fade = exp2_raw(static_cast<float>(all));
-    }
     lds_barrier();
-    if (i + 1 < end - first) fetch(ADJ ? tile - 1 : tile + 1);
-    if (!ADJ && i > 0) save(a.ws_tile + (unit * tiles + tile) * (N * P));
-    add_tile<NI, L, N>(
-        S, lds.b, lds.x, lds.fade,
-        [&](int t) { return ADJ ? lds.tk.from_state(t) : lds.tk.into_state(t); }, wave, g, c);
+    const Tokens<L>& tk = lds.tk[i & 1];
+    fetch(i + 1);
+    if (wave == 0 && i + 1 < n) total += lds.tk[(i + 1) & 1].fill(step, ah, lane);
+    step = steps_of(i + 2);
+    if (!ADJ && i > 0) save(a.ws_tile + (unit * tiles + first + i) * (N * P));
+    if constexpr (ADJ) add_tile(S, lds.b, 0, lds.x, wave, tk.fade, tk.head, g, c);
+    else add_tile(S, lds.b, 0, lds.x, wave, tk.fade, tk.into, g, c);
     lds_barrier();
   }
   if (ADJ) {
     save(a.ws_adj + (unit * f.segs + seg) * (N * P));
   } else {
-    save(f.ws_state + (unit * (f.segs + 1) + seg) * (N * P));
+    save(f.ws_state + (unit * f.segs + seg) * (N * P));
     if (tid == 0) f.ws_fade[unit * f.segs + seg] = total;
   }
 }
 
-// States in front of the segments (and behind the last), then adjoints behind them.
+template <int NI, int N>
+__global__ __launch_bounds__(NT, 2) void ttt_ssm_bwd_walk_k(SsmBackwardArgs a) {
+  __shared__ alignas(16) WalkLds<NI, N> lds;
+  const uint32_t forward = static_cast<uint32_t>(a.f.B) * a.f.H * a.f.segs;
+  if (blockIdx.x < forward) walk<NI, N, false>(a, lds, blockIdx.x);
+  else walk<NI, N, true>(a, lds, blockIdx.x - forward);
+}
+
+// States in front of the segments, and adjoints behind them.
 __global__ __launch_bounds__(NT) void ttt_ssm_bwd_join_k(SsmBackwardArgs a) {
   const SsmArgs& f = a.f;
   const int per = f.N * P / 4;
   const uint64_t i = static_cast<uint64_t>(blockIdx.x) * NT + threadIdx.x;
   const size_t unit = i / per, at = (i - unit * per) * 4, size = static_cast<size_t>(f.N) * P;
   const double* fades = f.ws_fade + unit * f.segs;
-  f32x4 S = {0.f, 0.f, 0.f, 0.f};
-  if (f.state0) S = *reinterpret_cast<const f32x4*>(f.state0 + unit * size + at);
-  float* p = f.ws_state + unit * (f.segs + 1) * size + at;
-  for (int s = 0; s < f.segs; ++s, p += size) {
-    const f32x4 added = *reinterpret_cast<const f32x4*>(p);
-    *reinterpret_cast<f32x4*>(p) = S;
-    S = S * exp2_raw(static_cast<float>(fades[s])) + added;
-  }
-  *reinterpret_cast<f32x4*>(p) = S;
-  f32x4 A = {0.f, 0.f, 0.f, 0.f};
-  if (a.dstate) A = *reinterpret_cast<const f32x4*>(a.dstate + unit * size + at);
-  p = a.ws_adj + (unit * f.segs + f.segs - 1) * size + at;
-  for (int s = f.segs - 1; s > 0; --s, p -= size) {
-    const f32x4 added = *reinterpret_cast<const f32x4*>(p);
-    *reinterpret_cast<f32x4*>(p) = A;
-    A = A * exp2_raw(static_cast<float>(fades[s])) + added;
-  }
-  *reinterpret_cast<f32x4*>(p) = A;
+  const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+  join_segments(f.ws_state + unit * f.segs * size + at, size, fades, f.segs, f.segs - 1, 1,
+                f.state0 ? *reinterpret_cast<const f32x4*>(f.state0 + unit * size + at) : zero);
+  join_segments(a.ws_adj + (unit * f.segs + f.segs - 1) * size + at, size, fades + f.segs - 1,
+                f.segs, f.segs - 1, -1,
+                a.dstate ? *reinterpret_cast<const f32x4*>(a.dstate + unit * size + at) : zero);
 }
 
 // ---- the gradients ----------------------------------------------------------
@@ -155,173 +153,157 @@ struct GradLds {
   static constexpr int NM = NI == 1 ? 2 : 3;   // parts of W1 and W2, and of A for dX
   Plane<NI, L, P> x, dy;
   Plane<NI, L, N> b, c;
-  Plane<3, P, N> adj;             // A behind the tile: row = feature of x, column = state row
-  Blocks<NM, BLOCKS> w1, w2, w2t; // [t, s], [t, s] and [s, t] with dt_s
-  Tokens<L> tk;
-  float u[4][L], v[4][L];         // per wave: u and v of its state rows
-  float zrow[BLOCKS][16], zcol[BLOCKS][16], zdiag[L];   // sums of Z by blocks; its diagonal
-  float dot[4];                   // per wave: <S, A> of its state rows
-  float fade, before;             // of the tile; from the segment's start to the tile
+  union {
+    Plane<3, P, N> adj;         // A behind the tile: row = feature of x, column = state row
+    struct {
+      Plane<NM, L, L> w1, w2;   // row = t, column = s
+    };
+  };
+  Tokens<L> tk[2];              // of even and odd tiles
+  // of even and odd tiles: u and v by the waves' state rows; sums of Z by
+  // blocks and its diagonal; <S, A> by the waves' state rows
+  float u[2][4][L], v[2][4][L], zrow[2][BLOCKS][16], zcol[2][BLOCKS][16], zdiag[2][L], dot[2][4];
+  float before;                 // decay from the segment's start to the tile
+  float dd[GT / 64];
 };
 
 template <int NI, int N>
-__global__ __launch_bounds__(NT) void ttt_ssm_bwd_k(SsmBackwardArgs a) {
+__global__ __launch_bounds__(GT, NI == 1 && N <= 64 ? 4 : 2) void ttt_ssm_bwd_k(
+    SsmBackwardArgs a) {
   using Lds = GradLds<NI, N>;
-  constexpr int L = Lds::L, TB = Lds::TB, NM = Lds::NM;
-  constexpr int NB = N >= 64 ? N / 64 : 1;   // state row blocks of a wave (N = 32: waves 0 and 1)
+  constexpr int L = Lds::L, TB = Lds::TB, NM = Lds::NM, JN = TB / 2, NA = N / 32;
+  constexpr int NB = N >= 64 ? N / 64 : 1;   // state row blocks of a wave (N = 32: waves 0, 1, 4, 5)
   __shared__ alignas(16) Lds lds;
   const SsmArgs& f = a.f;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, c = lane & 15;
-  const int seg = blockIdx.x % f.segs;
-  const size_t unit = blockIdx.x / f.segs;
-  const int h = static_cast<int>(unit % f.H);
-  const size_t shared = unit / f.H * f.G + h / (f.H / f.G);
+  const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, c = lane & 15;
+  const int full_wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wave = full_wave & 3, half = full_wave >> 2;
+  const Place at(f, blockIdx.x, f.segs);
+  const int seg = at.seg;
+  const size_t unit = at.unit, shared = at.shared;
   const int tiles = (f.T + L - 1) / L;
   const int first = seg * f.seg_tiles, end = min(first + f.seg_tiles, tiles);
-  const float ah = f.a[h], skip = f.d_skip ? f.d_skip[h] : 0.f;
+  const float ah = f.a[at.h], skip = f.d_skip ? f.d_skip[at.h] : 0.f;
   const bool has_rows = N >= 64 || wave < N / 16;
+  auto block = [&](int jj) { return TB == 4 ? (half ? 1 + jj : 3 * jj) : half; };   // of tokens
+  const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
 
-  // A behind the segment
-  f32x4 A[N / 16];
+  // A behind the segment: rows 16 (half NA + i) .., features 16 wave ..
+  f32x4 A[NA];
   {
     const float* from = a.ws_adj + (unit * f.segs + seg) * (N * P);
 #pragma unroll
-    for (int i = 0; i < N / 16; ++i)
+    for (int i = 0; i < NA; ++i)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) A[i][r] = from[(16 * i + 4 * g + r) * P + 16 * wave + c];
+      for (int r = 0; r < 4; ++r)
+        A[i][r] = from[(16 * (half * NA + i) + 4 * g + r) * P + 16 * wave + c];
   }
-  // a state by rows: row 16 (wave + 4 nb) + c, features by lane
-  struct Rows {
-    f32x4 v[NB][P / 32][2];
+  // a state by rows: row 16 (wave + 4 nb) + c, features 32 k + 16 hh + 4 g .. of lane (g, c)
+  auto row_of = [&](const float* p, int nb, int k, int hh) {
+    return *reinterpret_cast<const f32x4*>(p + (16 * (wave + 4 * nb) + c) * P + 32 * k + 16 * hh +
+                                           4 * g);
   };
-  auto load_rows = [&](const float* p) {
-    Rows r;
+  const float* seg_state = f.ws_state + (unit * f.segs + seg) * (N * P);
+  double rest = f.ws_fade[unit * f.segs + seg];   // log2 decay from the segment's start
+  float dd_sum = 0.f;
+  double da_sum = 0.0;
+
+  Fetch<NI, L, P, GT> fx, fy;
+  Fetch<NI, L, N, GT> fb, fc;
+  auto valid_of = [&](int tile) { return tile >= first ? min(L, f.T - tile * L) : 0; };
+  auto fetch = [&](int tile) {
+    const int t0 = tile * L, valid = valid_of(tile);
+    fx.load(row_ptr<NI>(f.x, unit * f.T + t0, P), valid, tid);
+    fy.load(row_ptr<NI>(a.dy, unit * f.T + t0, P), valid, tid);
+    fb.load(row_ptr<NI>(f.b, shared * f.T + t0, N), valid, tid);
+    fc.load(row_ptr<NI>(f.c, shared * f.T + t0, N), valid, tid);
+  };
+  auto steps_of = [&](int tile) {
+    return load_steps(f.dt + unit * f.T + tile * L, valid_of(tile), lane);
+  };
+  // ddt of a tile whose sums stand in LDS, and its share of da; by one wave
+  auto finish = [&](int tile) {
+    const int e = tile & 1, valid = valid_of(tile);
+    const Tokens<L>& tk = lds.tk[e];
+    double after = 0.0, upto = 0.0;   // of the token: u + row - column sums of Z; dt v
+    float dt = 0.f, direct = 0.f;
+    if (lane < L) {
+      dt = tk.dt[lane];
+      const float us = (lds.u[e][0][lane] + lds.u[e][1][lane]) +
+                       (lds.u[e][2][lane] + lds.u[e][3][lane]);
+      const float vs = (lds.v[e][0][lane] + lds.v[e][1][lane]) +
+                       (lds.v[e][2][lane] + lds.v[e][3][lane]);
+      float row = 0.f, col = 0.f;
+      const int mine = lane >> 4, in = lane & 15;
+#pragma unroll
+      for (int k = 0; k < TB; ++k) {
+        if (k <= mine) row += lds.zrow[e][mine * (mine + 1) / 2 + k][in];
+        if (k >= mine) col += lds.zcol[e][k * (k + 1) / 2 + mine][in];
+      }
+      after = static_cast<double>(us) + row - static_cast<double>(dt) * col;
+      upto = static_cast<double>(dt) * vs;
+      direct = vs + (col + lds.zdiag[e][lane]);
+    }
+    const double after_to = wave_scan(after), upto_to = wave_scan(upto);
+    const float d = (lds.dot[e][0] + lds.dot[e][1]) + (lds.dot[e][2] + lds.dot[e][3]);
+    const double ex = (last_lane(after_to) - after_to + after) + (upto_to - upto) + tk.fade * d;
+    if (lane < valid) {
+      a.ddt[unit * f.T + tile * L + lane] = static_cast<float>(direct + ah * ex);
+      da_sum += dt * ex;
+    }
+  };
+
+  fetch(end - 1);
+  float step = steps_of(end - 1);
+  if (full_wave == 7) {
+    rest -= lds.tk[(end - 1) & 1].fill(step, ah, lane);
+    if (lane == 0) lds.before = exp2_raw(static_cast<float>(rest));
+  }
+  step = steps_of(end - 2);
+  for (int tile = end - 1; tile >= first; --tile) {
+    const int t0 = tile * L, valid = valid_of(tile), e = tile & 1;
+    const Tokens<L>& tk = lds.tk[e];
+    // the segment's own part of the state before the tile
+    f32x4 own[NB][P / 32][2];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
       for (int k = 0; k < P / 32; ++k)
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh)
-          r.v[nb][k][hh] = has_rows ? *reinterpret_cast<const f32x4*>(
-                                          p + (16 * (wave + 4 * nb) + c) * P + 32 * k + 16 * hh + 4 * g)
-                                    : f32x4{0.f, 0.f, 0.f, 0.f};
-    return r;
-  };
-  const float* seg_state = f.ws_state + (unit * (f.segs + 1) + seg) * (N * P);
-  double rest = f.ws_fade[unit * f.segs + seg];   // log2 decay from the segment's start
-  float dd_sum = 0.f;
-  double da_sum = 0.0;
-
-  Fetch<NI, L, P, NT> fx, fy;
-  Fetch<NI, L, N, NT> fb, fc;
-  float step = 0.f;
-  auto fetch = [&](int tile) {
-    const int t0 = tile * L, valid = min(L, f.T - t0);
-    fx.load(row_ptr<NI>(f.x, unit * f.T + t0, P), valid, tid);
-    fy.load(row_ptr<NI>(a.dy, unit * f.T + t0, P), valid, tid);
-    fb.load(row_ptr<NI>(f.b, shared * f.T + t0, N), valid, tid);
-    fc.load(row_ptr<NI>(f.c, shared * f.T + t0, N), valid, tid);
-    step = lane < valid ? f.dt[unit * f.T + t0 + lane] : 0.f;
-  };
-  fetch(end - 1);
-  for (int tile = end - 1; tile >= first; --tile) {
-    const int t0 = tile * L, valid = min(L, f.T - t0);
+          own[nb][k][hh] = has_rows && tile > first
+                               ? row_of(a.ws_tile + (unit * tiles + tile) * (N * P), nb, k, hh)
+                               : zero;
     fx.store(lds.x, tid);
     fy.store(lds.dy, tid);
     fb.store(lds.b, tid);
     fc.store(lds.c, tid);
-    if (wave == 0) {
-      const double all = lds.tk.fill(step, ah, lane);
-      rest -= all;
-      if (lane == 0) {
-        lds.fade = exp2_raw(static_cast<float>(all));
-        lds.before = exp2_raw(static_cast<float>(rest));
-      }
-    }
 #pragma unroll
-    for (int i = 0; i < N / 16; ++i) {
+    for (int i = 0; i < NA; ++i) {
       u32x2 p[3];
       split_parts<3>(A[i], p);
 #pragma unroll
       for (int k = 0; k < 3; ++k)
-        *reinterpret_cast<u32x2*>(&lds.adj.v[k][16 * wave + c][16 * i + 4 * g]) = p[k];
+        lds.adj.put4(k, 16 * wave + c, 16 * (half * NA + i) + 4 * g, p[k]);
     }
     lds_barrier();
-    if (tile > first) fetch(tile - 1);
-    // the state before the tile: the segment's own part and what came in front of it
-    Rows S = load_rows(seg_state);
-    {
-      const float w = lds.before;
-      if (tile > first) {
-        const Rows own = load_rows(a.ws_tile + (unit * tiles + tile) * (N * P));
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-          for (int k = 0; k < P / 32; ++k)
-#pragma unroll
-            for (int hh = 0; hh < 2; ++hh)
-              S.v[nb][k][hh] = S.v[nb][k][hh] * w + own.v[nb][k][hh];
-      }
-    }
-
-    // W1, W2 and W2^T block by block
-    for (int i = wave; i < Lds::BLOCKS; i += 4) {
-      int tb, sb;
-      block_of(i, &tb, &sb);
-      f32x4 w1 = {0.f, 0.f, 0.f, 0.f}, w2 = w1, w2t = w1;
-#pragma unroll
-      for (int k = 0; k < N / 32; ++k)
-        w1 = mfma_parts(lds.c.rows8(16 * tb, 32 * k, g, c), lds.b.rows8(16 * sb, 32 * k, g, c),
-                        w1);
-#pragma unroll
-      for (int k = 0; k < P / 32; ++k) {
-        const Parts<NI> yr = lds.dy.rows8(16 * tb, 32 * k, g, c);
-        const Parts<NI> xr = lds.x.rows8(16 * sb, 32 * k, g, c);
-        w2 = mfma_parts(yr, xr, w2);
-        w2t = mfma_parts(xr, yr, w2t);
-      }
-      float col = 0.f;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        if (tb == sb && 4 * g + r == c) dd_sum += w2[r];
-        {
-          const int t = 16 * tb + 4 * g + r, s = 16 * sb + c;
-          const float fade = lds.tk.fade(t, s);
-          w1[r] = s <= t ? w1[r] * fade : 0.f;
-          const float z = w1[r] * w2[r];
-          w2[r] = s <= t ? w2[r] * fade : 0.f;
-          const float row = row_sum16(s < t ? z * lds.tk.dt[s] : 0.f);
-          if (c == r) lds.zrow[i][4 * g + r] = row;
-          if (s == t) lds.zdiag[t] = z;
-          else col += s < t ? z : 0.f;
-        }
-        {
-          const int t = 16 * tb + c, s = 16 * sb + 4 * g + r;
-          w2t[r] = s <= t ? w2t[r] * (lds.tk.fade(t, s) * lds.tk.dt[s]) : 0.f;
-        }
-      }
-      col = group_sum(col);
-      if (g == 0) lds.zcol[i][c] = col;
-      lds.w1.put(i, lane, w1);
-      lds.w2.put(i, lane, w2);
-      lds.w2t.put(i, lane, w2t);
-    }
+    const float before = lds.before;
+    fetch(tile - 1);
 
     // what the adjoint behind the tile and the state before it give
-    f32x4 dx[TB], db[NB][TB], dc[NB][TB];
-    const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+    f32x4 dx[JN], db[NB][JN], dc[NB][JN];
 #pragma unroll
-    for (int j = 0; j < TB; ++j) {
-      dx[j] = zero;
+    for (int jj = 0; jj < JN; ++jj) {
+      dx[jj] = zero;
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) db[nb][j] = dc[nb][j] = zero;
+      for (int nb = 0; nb < NB; ++nb) db[nb][jj] = dc[nb][jj] = zero;
     }
 #pragma unroll
     for (int k = 0; k < N / 32; ++k) {
-      const Parts<NM> ap = split_frag<NM>(A[2 * k], A[2 * k + 1]);
+      const Parts<NM> ap = lds.adj.template rows<NM>(16 * wave, 32 * k, g, c);
 #pragma unroll
-      for (int j = 0; j < TB; ++j)
-        dx[j] = mfma_parts(ap, lds.b.rows(16 * j, 32 * k, g, c), dx[j]);
+      for (int jj = 0; jj < JN; ++jj)
+        dx[jj] = mfma_parts(ap, lds.b.rows(16 * block(jj), 32 * k, g, c), dx[jj]);
     }
     float dot = 0.f;
     if (has_rows) {
@@ -329,175 +311,205 @@ __global__ __launch_bounds__(NT) void ttt_ssm_bwd_k(SsmBackwardArgs a) {
       for (int k = 0; k < P / 32; ++k) {
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
+          // what came in front of the segment
+          f32x4 S[2] = {row_of(seg_state, nb, k, 0), row_of(seg_state, nb, k, 1)};
           const Parts<3> ar = lds.adj.cols(32 * k, 16 * (wave + 4 * nb), g, c);
 #pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            const f32x4 prod = frag_half(ar, hh) * S.v[nb][k][hh];
-            dot += (prod[0] + prod[1]) + (prod[2] + prod[3]);
-          }
-          const Parts<3> sp = split_frag<3>(S.v[nb][k][0], S.v[nb][k][1]);
+          for (int jj = 0; jj < JN; ++jj)
+            db[nb][jj] =
+                mfma_parts(ar, lds.x.rows(16 * block(jj), 32 * k, g, c), db[nb][jj]);
 #pragma unroll
-          for (int j = 0; j < TB; ++j) {
-            db[nb][j] = mfma_parts(ar, lds.x.rows(16 * j, 32 * k, g, c), db[nb][j]);
-            dc[nb][j] = mfma_parts(sp, lds.dy.rows(16 * j, 32 * k, g, c), dc[nb][j]);
+          for (int hh = 0; hh < 2; ++hh) {
+            S[hh] = S[hh] * before + own[nb][k][hh];
+            if (half == 0) {
+              const f32x4 prod = frag_half(ar, hh) * S[hh];
+              dot += (prod[0] + prod[1]) + (prod[2] + prod[3]);
+            }
           }
+          const Parts<3> sp = split_frag<3>(S[0], S[1]);
+#pragma unroll
+          for (int jj = 0; jj < JN; ++jj)
+            dc[nb][jj] =
+                mfma_parts(sp, lds.dy.rows(16 * block(jj), 32 * k, g, c), dc[nb][jj]);
         }
       }
     }
-    dot = wave_sum(dot);
-    if (lane == 0) lds.dot[wave] = dot;
+    if (half == 0) {
+      dot = wave_sum(dot);
+      if (lane == 0) lds.dot[e][wave] = dot;
+    }
 #pragma unroll
-    for (int j = 0; j < TB; ++j) {
-      const int t = 16 * j + c;
-      dx[j] *= lds.tk.tail[t];
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        db[nb][j] *= lds.tk.tail[t];
-        dc[nb][j] *= lds.tk.head[t];
-      }
+    for (int jj = 0; jj < JN; ++jj) {
+      const int t = 16 * block(jj) + c;
+      const float into = tk.into[t], head = tk.head[t];
       float us = 0.f, vs = 0.f;
       if (has_rows) {
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
           const int n = 16 * (wave + 4 * nb) + 4 * g;
-          const f32x4 pv = lds.b.four(t, n) * db[nb][j], pu = lds.c.four(t, n) * dc[nb][j];
+          const f32x4 pv = lds.b.four(t, n) * db[nb][jj], pu = lds.c.four(t, n) * dc[nb][jj];
           vs += (pv[0] + pv[1]) + (pv[2] + pv[3]);
           us += (pu[0] + pu[1]) + (pu[2] + pu[3]);
+          db[nb][jj] *= into;
+          dc[nb][jj] *= head;
         }
       }
-      us = group_sum(us);
-      vs = group_sum(vs);
+      dx[jj] *= into;
+      us = group_sum(us) * head;
+      vs = group_sum(vs) * tk.tail[t];
       if (g == 0) {
-        lds.u[wave][t] = us;
-        lds.v[wave][t] = vs;
+        lds.u[e][wave][t] = us;
+        lds.v[e][wave][t] = vs;
+      }
+    }
+    if (full_wave == 7) {   // the tile behind is done, the one before is next
+      if (tile < end - 1) finish(tile + 1);
+      if (tile > first) rest -= lds.tk[e ^ 1].fill(step, ah, lane);
+    }
+    step = steps_of(tile - 2);
+    lds_barrier();
+    if (full_wave == 7 && lane == 0) lds.before = exp2_raw(static_cast<float>(rest));
+
+    // W1 and W2 block by block
+    for (int i = full_wave; i < Lds::BLOCKS; i += GT / 64) {
+      int tb, sb;
+      block_of(i, &tb, &sb);
+      f32x4 gt = zero, xt = zero;   // rows s, columns t
+#pragma unroll
+      for (int k = 0; k < N / 32; ++k)
+        gt = mfma_parts(lds.b.rows8(16 * sb, 32 * k, g, c), lds.c.rows8(16 * tb, 32 * k, g, c),
+                        gt);
+#pragma unroll
+      for (int k = 0; k < P / 32; ++k)
+        xt = mfma_parts(lds.x.rows8(16 * sb, 32 * k, g, c), lds.dy.rows8(16 * tb, 32 * k, g, c),
+                        xt);
+      const int t = 16 * tb + c, s0 = 16 * sb + 4 * g;
+      const f32x4 fade = tk.fades(tb, t, s0), dt = tk.steps(s0);
+      const f32x4 z = gt * xt * fade;
+      f32x4 w1 = gt * (fade * dt), w2 = xt * (fade * dt);
+      float row = 0.f;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const bool diagonal = tb == sb && 4 * g + r == c;
+        if (diagonal) {
+          lds.zdiag[e][t] = z[r];
+          dd_sum += xt[r];
+          w1[r] += skip;
+        }
+        const float off = diagonal ? 0.f : z[r];
+        row += off * dt[r];
+        const float col = row_sum16(off);
+        if (c == r) lds.zcol[e][i][4 * g + r] = col;
+      }
+      row = group_sum(row);
+      if (g == 0) lds.zrow[e][i][c] = row;
+      u32x2 p[NM], q[NM];
+      split_parts<NM>(w1, p);
+      split_parts<NM>(w2, q);
+#pragma unroll
+      for (int k = 0; k < NM; ++k) {
+        lds.w1.put4(k, t, s0, p[k]);
+        lds.w2.put4(k, t, s0, q[k]);
+      }
+    }
+    // the blocks above the diagonal that a product of 32 tokens meets
+    if (full_wave >= 8 - JN) {
+      const int t = 32 * (full_wave - (8 - JN)) + c, s0 = t - c + 16 + 4 * g;
+#pragma unroll
+      for (int k = 0; k < NM; ++k) {
+        lds.w1.put4(k, t, s0, u32x2{0u, 0u});
+        lds.w2.put4(k, t, s0, u32x2{0u, 0u});
       }
     }
     lds_barrier();
 
     // and the tile's own tokens
-    auto pair = [&](const Blocks<NM, Lds::BLOCKS>& w, int i0, int i1) {   // -1: zero
-      Parts<NM> m;
-#pragma unroll
-      for (int p = 0; p < NM; ++p)
-        m.p[p] = cat(i0 >= 0 ? w.v[i0][p][lane] : u32x2{0u, 0u},
-                     i1 >= 0 ? w.v[i1][p][lane] : u32x2{0u, 0u});
-      return m;
-    };
-    auto at = [](int tb, int sb) { return sb <= tb ? tb * (tb + 1) / 2 + sb : -1; };
 #pragma unroll
     for (int k = 0; k < L / 32; ++k) {
       const Parts<NI> yt = lds.dy.cols(32 * k, 16 * wave, g, c);
 #pragma unroll
-      for (int j = 0; j <= 2 * k + 1; ++j)
-        dx[j] = mfma_parts(yt, pair(lds.w1, at(2 * k, j), at(2 * k + 1, j)), dx[j]);
+      for (int jj = 0; jj < JN; ++jj)
+        if (block(jj) <= 2 * k + 1)
+          dx[jj] = mfma_parts(yt, lds.w1.cols(32 * k, 16 * block(jj), g, c), dx[jj]);
       if (has_rows) {
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
           const Parts<NI> ct = lds.c.cols(32 * k, 16 * (wave + 4 * nb), g, c);
           const Parts<NI> bt = lds.b.cols(32 * k, 16 * (wave + 4 * nb), g, c);
 #pragma unroll
-          for (int j = 0; j <= 2 * k + 1; ++j)
-            db[nb][j] = mfma_parts(ct, pair(lds.w2, at(2 * k, j), at(2 * k + 1, j)), db[nb][j]);
-#pragma unroll
-          for (int j = 2 * k; j < TB; ++j)
-            dc[nb][j] = mfma_parts(bt, pair(lds.w2t, at(j, 2 * k), at(j, 2 * k + 1)), dc[nb][j]);
-        }
-      }
-    }
-
-    // stores
-#pragma unroll
-    for (int j = 0; j < TB; ++j) {
-      const int t = 16 * j + c;
-      const float dt = lds.tk.dt[t];
-      {
-        f32x4 v = dx[j] * dt;
-        if (f.d_skip) v += lds.dy.four(t, 16 * wave + 4 * g) * skip;
-        if (t < valid) {
-          const size_t o = (unit * f.T + t0 + t) * P + 16 * wave + 4 * g;
-          if constexpr (NI == 1)
-            *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.dx) + o) =
-                u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
-          else
-            *reinterpret_cast<f32x4*>(static_cast<float*>(a.dx) + o) = v;
-        }
-      }
-      if (has_rows && t < valid) {
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          const int n = 16 * (wave + 4 * nb) + 4 * g;
-          const f32x4 v = db[nb][j] * dt;
-          if (a.ws_db) {
-            const size_t o = (unit * f.T + t0 + t) * N + n;
-            *reinterpret_cast<f32x4*>(a.ws_db + o) = v;
-            *reinterpret_cast<f32x4*>(a.ws_dc + o) = dc[nb][j];
-          } else {
-            const size_t o = (shared * f.T + t0 + t) * N + n;
-            if constexpr (NI == 1) {
-              *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.db) + o) =
-                  u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
-              *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.dc) + o) =
-                  u32x2{pack_bf16(dc[nb][j][0], dc[nb][j][1]),
-                        pack_bf16(dc[nb][j][2], dc[nb][j][3])};
-            } else {
-              *reinterpret_cast<f32x4*>(static_cast<float*>(a.db) + o) = v;
-              *reinterpret_cast<f32x4*>(static_cast<float*>(a.dc) + o) = dc[nb][j];
-            }
+          for (int jj = 0; jj < JN; ++jj) {
+            if (block(jj) <= 2 * k + 1)
+              db[nb][jj] =
+                  mfma_parts(ct, lds.w2.cols(32 * k, 16 * block(jj), g, c), db[nb][jj]);
+            if (block(jj) >= 2 * k)
+              dc[nb][jj] =
+                  mfma_parts(bt, lds.w2.rows(16 * block(jj), 32 * k, g, c), dc[nb][jj]);
           }
         }
       }
     }
 
-    // A before the tile
-    add_tile<NI, L, N>(
-        A, lds.c, lds.dy, lds.fade, [&](int t) { return lds.tk.from_state(t); }, wave, g, c);
-    lds_barrier();
-
-    if (wave == 0) {   // ddt, and the tile's share of da
-      double after = 0.0, upto = 0.0;   // of the token: u + row - column sums of Z; dt v
-      float dt = 0.f, direct = 0.f;
-      if (lane < L) {
-        dt = lds.tk.dt[lane];
-        const float us = (lds.u[0][lane] + lds.u[1][lane]) + (lds.u[2][lane] + lds.u[3][lane]);
-        const float vs = (lds.v[0][lane] + lds.v[1][lane]) + (lds.v[2][lane] + lds.v[3][lane]);
-        float row = 0.f, col = 0.f;
-        const int mine = lane >> 4, in = lane & 15;
+    constexpr int ES = NI == 1 ? 2 : 4;
+    const __amdgpu_buffer_rsrc_t out =
+        rows_of(row_ptr<NI>(a.dx, unit * f.T + t0, P), valid * P * ES);
 #pragma unroll
-        for (int k = 0; k < TB; ++k) {
-          if (k <= mine) row += lds.zrow[mine * (mine + 1) / 2 + k][in];
-          if (k >= mine) col += lds.zcol[k * (k + 1) / 2 + mine][in];
-        }
-        after = static_cast<double>(us) + row - static_cast<double>(dt) * col;
-        upto = static_cast<double>(dt) * vs;
-        direct = vs + (col + lds.zdiag[lane]);
-      }
-      const double after_to = wave_scan(after), upto_to = wave_scan(upto);
-      const float d = (lds.dot[0] + lds.dot[1]) + (lds.dot[2] + lds.dot[3]);
-      const double e = (last_lane(after_to) - after_to + after) + (upto_to - upto) + lds.fade * d;
-      if (lane < valid) {
-        a.ddt[unit * f.T + t0 + lane] = static_cast<float>(direct + ah * e);
-        da_sum += dt * e;
+    for (int jj = 0; jj < JN; ++jj)
+      store_row4<NI>(out, 16 * block(jj) + c, P, 16 * wave + 4 * g, dx[jj]);
+    if (has_rows) {
+      if (a.ws_db) {   // of this head alone, in fp32
+        const size_t o = (unit * f.T + t0) * N;
+        const __amdgpu_buffer_rsrc_t ob = rows_of(a.ws_db + o, valid * N * 4);
+        const __amdgpu_buffer_rsrc_t oc = rows_of(a.ws_dc + o, valid * N * 4);
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int jj = 0; jj < JN; ++jj) {
+            const int t = 16 * block(jj) + c, n = 16 * (wave + 4 * nb) + 4 * g;
+            store_row4<3>(ob, t, N, n, db[nb][jj]);
+            store_row4<3>(oc, t, N, n, dc[nb][jj]);
+          }
+      } else {
+        const __amdgpu_buffer_rsrc_t ob =
+            rows_of(row_ptr<NI>(a.db, shared * f.T + t0, N), valid * N * ES);
+        const __amdgpu_buffer_rsrc_t oc =
+            rows_of(row_ptr<NI>(a.dc, shared * f.T + t0, N), valid * N * ES);
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int jj = 0; jj < JN; ++jj) {
+            const int t = 16 * block(jj) + c, n = 16 * (wave + 4 * nb) + 4 * g;
+            store_row4<NI>(ob, t, N, n, db[nb][jj]);
+            store_row4<NI>(oc, t, N, n, dc[nb][jj]);
+          }
       }
     }
+
+    // A before the tile
+    add_tile(A, lds.c, half * NA, lds.dy, wave, tk.fade, tk.head, g, c);
+    lds_barrier();
   }
+  if (full_wave == 7) finish(first);
   if (a.dstate0 && seg == 0) {
     float* out = a.dstate0 + unit * (N * P);
 #pragma unroll
-    for (int i = 0; i < N / 16; ++i)
+    for (int i = 0; i < NA; ++i)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) out[(16 * i + 4 * g + r) * P + 16 * wave + c] = A[i][r];
+      for (int r = 0; r < 4; ++r)
+        out[(16 * (half * NA + i) + 4 * g + r) * P + 16 * wave + c] = A[i][r];
   }
   // the segment's da and dd
   dd_sum = wave_sum(dd_sum);
+  if (lane == 0) lds.dd[full_wave] = dd_sum;
   lds_barrier();
-  if (lane == 0) lds.dot[wave] = dd_sum;
-  lds_barrier();
-  if (wave == 0) {
+  if (full_wave == 7) {
     const double all = last_lane(wave_scan(da_sum));
     if (lane == 0) {
       float* out = a.ws_sums + (unit * f.segs + seg) * 2;
+      float dd = 0.f;
+#pragma unroll
+      for (int k = 0; k < GT / 64; ++k) dd += lds.dd[k];
       out[0] = static_cast<float>(all);
-      out[1] = (lds.dot[0] + lds.dot[1]) + (lds.dot[2] + lds.dot[3]);
+      out[1] = dd;
     }
   }
 }
@@ -554,17 +566,12 @@ hipError_t bwd_launch(const SsmBackwardArgs& a, hipStream_t stream) {
   const SsmArgs& f = a.f;
   const uint32_t units = static_cast<uint32_t>(f.B) * f.H;
   hipError_t e;
-  hipLaunchKernelGGL((ttt_ssm_bwd_walk_k<NI, N, false>), dim3(units * f.segs), dim3(NT), 0, stream,
-                     a);
+  hipLaunchKernelGGL((ttt_ssm_bwd_walk_k<NI, N>), dim3(units * (2 * f.segs - 1)), dim3(NT), 0,
+                     stream, a);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  if (f.segs > 1) {
-    hipLaunchKernelGGL((ttt_ssm_bwd_walk_k<NI, N, true>), dim3(units * (f.segs - 1)), dim3(NT), 0,
-                       stream, a);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-  }
   hipLaunchKernelGGL(ttt_ssm_bwd_join_k, dim3(units * (N * P / 4 / NT)), dim3(NT), 0, stream, a);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  hipLaunchKernelGGL((ttt_ssm_bwd_k<NI, N>), dim3(units * f.segs), dim3(NT), 0, stream, a);
+  hipLaunchKernelGGL((ttt_ssm_bwd_k<NI, N>), dim3(units * f.segs), dim3(GT), 0, stream, a);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   hipLaunchKernelGGL(ttt_ssm_bwd_sum_k, dim3(f.H), dim3(64), 0, stream, a);
   if ((e = hipGetLastError()) != hipSuccess) return e;

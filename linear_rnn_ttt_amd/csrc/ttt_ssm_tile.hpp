@@ -23,7 +23,6 @@ namespace tttk {
 
 constexpr int SSM_P = 64;     // features of x per head
 constexpr int SSM_NT = 256;   // threads of a workgroup: four waves of 16 features
-constexpr int SSM_PAD = 8;    // bf16 added to every LDS row: 16 rows hit 16 different 16-byte banks
 
 template <int N>
 struct Parts {
@@ -84,19 +83,33 @@ __device__ __forceinline__ f32x4 frag_half(const Parts<NP>& f, int h) {
   return x;
 }
 
-// L tokens x W features as NI planes of bf16 parts.
+// L tokens x W features as NI planes of bf16 parts.  The 16-byte chunk q of row
+// t sits at chunk q ^ swizzle(t), so that the 16 rows of a fragment spread over
+// the banks without padding (which would cost the scan its fourth workgroup
+// per compute unit).
 template <int NI, int L, int W>
 struct Plane {
-  uint16_t v[NI][L][W + SSM_PAD];
+  uint16_t v[NI][L][W];
+
+  static __device__ __forceinline__ int swizzle(int t) { return W >= 64 ? t & 7 : (t >> 1) & 3; }
+  // where feature f (a multiple of 4) of token t sits in its row
+  static __device__ __forceinline__ int place(int t, int f) {
+    return (((f >> 3) ^ swizzle(t)) << 3) | (f & 4);
+  }
+  __device__ __forceinline__ u32x2 get4(int p, int t, int f) const {
+    return *reinterpret_cast<const u32x2*>(&v[p][t][place(t, f)]);
+  }
+  __device__ __forceinline__ void put4(int p, int t, int f, u32x2 x) {
+    *reinterpret_cast<u32x2*>(&v[p][t][place(t, f)]) = x;
+  }
 
   // Rows t0 + c, features f0 + {4 g .. 4 g + 3, 16 + 4 g .. 16 + 4 g + 3}.
-  __device__ __forceinline__ Parts<NI> rows(int t0, int f0, int g, int c) const {
-    Parts<NI> r;
+  template <int NP = NI>
+  __device__ __forceinline__ Parts<NP> rows(int t0, int f0, int g, int c) const {
+    Parts<NP> r;
 #pragma unroll
-    for (int p = 0; p < NI; ++p) {
-      const uint16_t* s = &v[p][t0 + c][f0 + 4 * g];
-      r.p[p] = cat(*reinterpret_cast<const u32x2*>(s), *reinterpret_cast<const u32x2*>(s + 16));
-    }
+    for (int p = 0; p < NP; ++p)
+      r.p[p] = cat(get4(p, t0 + c, f0 + 4 * g), get4(p, t0 + c, f0 + 16 + 4 * g));
     return r;
   }
   // The same rows with features f0 + 8 g .. 8 g + 7 (one 16-byte read): for
@@ -105,7 +118,7 @@ struct Plane {
     Parts<NI> r;
 #pragma unroll
     for (int p = 0; p < NI; ++p)
-      r.p[p] = *reinterpret_cast<const u32x4*>(&v[p][t0 + c][f0 + 8 * g]);
+      r.p[p] = *reinterpret_cast<const u32x4*>(&v[p][t0 + c][place(t0 + c, f0 + 8 * g)]);
     return r;
   }
   // Feature f0 + c, tokens t0 + {4 g .. 4 g + 3, 16 + 4 g .. 16 + 4 g + 3}: the
@@ -115,12 +128,13 @@ struct Plane {
     typedef short s16x4l __attribute__((ext_vector_type(4)));
     typedef __attribute__((address_space(3))) s16x4l* lp;
     Parts<NI> r;
+    const int t = t0 + 4 * g + (c >> 2), f = place(t, f0 + 4 * (c & 3));   // t + 16: same swizzle
 #pragma unroll
     for (int p = 0; p < NI; ++p) {
-      const uint16_t* s = &v[p][t0 + 4 * g + (c >> 2)][f0 + 4 * (c & 3)];
-      const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)s));
+      const u32x2 lo = __builtin_bit_cast(
+          u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)&v[p][t][f]));
       const u32x2 hi = __builtin_bit_cast(
-          u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(s + 16 * (W + SSM_PAD))));
+          u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)&v[p][t + 16][f]));
       r.p[p] = cat(lo, hi);
     }
     return r;
@@ -129,44 +143,67 @@ struct Plane {
   __device__ __forceinline__ f32x4 four(int t, int f) const {
     f32x4 x = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int p = NI - 1; p >= 0; --p) x += widen4(*reinterpret_cast<const u32x2*>(&v[p][t][f]));
+    for (int p = NI - 1; p >= 0; --p) x += widen4(get4(p, t, f));
     return x;
   }
 };
+
+// A range of memory for buffer loads and stores: reads past `bytes` give zero,
+// stores past it do nothing, so a tile's missing rows need no branches.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(const void* p, int bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), static_cast<short>(0), bytes,
+                                           0x00020000);
+}
 
 // A tile's rows on their way from memory: 16 bytes per vector, rows from
 // `valid` on are zero.
 template <int NI, int L, int W, int THREADS>
 struct Fetch {
   static constexpr int VE = NI == 1 ? 8 : 4;                 // values of a 16-byte vector
-  static constexpr int VECS = L * W / VE, PER = VECS / THREADS;
-  static_assert(VECS % THREADS == 0, "whole vectors per thread");
+  static constexpr int VECS = L * W / VE, PER = (VECS + THREADS - 1) / THREADS;
+  static constexpr int RB = W * (NI == 1 ? 2 : 4);           // bytes of a row
   u32x4 r[PER];
 
-  // src: the tile's first row ([L][W] contiguous)
+  // src: the tile's first row ([L][W] contiguous); nothing is read for valid <= 0
   __device__ __forceinline__ void load(const void* src, int valid, int tid) {
+    const __amdgpu_buffer_rsrc_t m = rows_of(src, max(valid, 0) * RB);
 #pragma unroll
-    for (int j = 0; j < PER; ++j) {
-      const int i = tid + THREADS * j;
-      r[j] = i * VE / W < valid ? static_cast<const u32x4*>(src)[i] : u32x4{0, 0, 0, 0};
-    }
+    for (int j = 0; j < PER; ++j)
+      r[j] = __builtin_bit_cast(
+          u32x4, __builtin_amdgcn_raw_buffer_load_b128(m, 16 * (tid + THREADS * j), 0, 0));
   }
   __device__ __forceinline__ void store(Plane<NI, L, W>& to, int tid) const {
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
       const int i = tid + THREADS * j;
+      if (VECS % THREADS != 0 && i >= VECS) break;
       const int row = i * VE / W, col = i * VE % W;
       if constexpr (NI == 1) {
-        *reinterpret_cast<u32x4*>(&to.v[0][row][col]) = r[j];
+        *reinterpret_cast<u32x4*>(&to.v[0][row][to.place(row, col)]) = r[j];
       } else {
         u32x2 p[NI];
         split_parts<NI>(__builtin_bit_cast(f32x4, r[j]), p);
 #pragma unroll
-        for (int k = 0; k < NI; ++k) *reinterpret_cast<u32x2*>(&to.v[k][row][col]) = p[k];
+        for (int k = 0; k < NI; ++k) to.put4(k, row, col, p[k]);
       }
     }
   }
 };
+
+// Four values of row t, feature f of a [.., W] array behind `m`: fp32, or
+// rounded once to bf16.
+template <int NI>
+__device__ __forceinline__ void store_row4(__amdgpu_buffer_rsrc_t m, int t, int W, int f,
+                                           f32x4 v) {
+  if constexpr (NI == 1) {
+    typedef uint32_t u32x2v __attribute__((ext_vector_type(2)));
+    __builtin_amdgcn_raw_buffer_store_b64(
+        u32x2v{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])}, m, (t * W + f) * 2, 0, 0);
+  } else {
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), m, (t * W + f) * 4, 0,
+                                           0);
+  }
+}
 
 // Inclusive sum over the wave's lanes (DPP row shifts, then row broadcasts).
 __device__ __forceinline__ double wave_scan(double v) {
@@ -189,52 +226,83 @@ __device__ __forceinline__ double wave_scan(double v) {
   return v;
 }
 
-__device__ __forceinline__ double last_lane(double v) {
+__device__ __forceinline__ double lane_of(double v, int lane) {
   const uint64_t b = __builtin_bit_cast(uint64_t, v);
-  const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(b & 0xffffffffu), 63);
-  const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(b >> 32), 63);
+  const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(b & 0xffffffffu), lane);
+  const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(b >> 32), lane);
   return __builtin_bit_cast(double, (static_cast<uint64_t>(hi) << 32) | lo);
 }
 
+__device__ __forceinline__ double last_lane(double v) { return lane_of(v, 63); }
+
 __device__ __forceinline__ float exp2_raw(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// The steps dt of a tile, lane = token; zero from `valid` on.
+__device__ __forceinline__ float load_steps(const float* dt, int valid, int lane) {
+  return __builtin_bit_cast(
+      float, __builtin_amdgcn_raw_buffer_load_b32(rows_of(dt, max(valid, 0) * 4), 4 * lane, 0, 0));
+}
+
 // Per-token values of a tile.  cum_t = log2(e) a (dt_0 + ... + dt_t) is summed
-// in fp64 and kept as hi + lo, so that a difference of two of them keeps
-// fp32's relative precision also behind a large step that resets the state.
+// in fp64, and every decay is made from a difference of two of them rounded
+// once, so that it keeps fp32's relative precision also behind a large step
+// that resets the state.  Decays between tokens of different 16-token blocks
+// are products of two factors that meet at the later block's start; those
+// within a block are made one by one from cum = hi + lo.
 template <int L>
 struct alignas(16) Tokens {
-  float hi[L], lo[L];   // cum
+  float hi[L], lo[L];        // cum
   float dt[L];
-  float head[L];        // exp2(cum_t): from the tile's start through token t
-  float tail[L];        // exp2(cum_last - cum_t): from token t to the tile's end
+  float head[L];             // exp2(cum_t): from the tile's start through token t
+  float tail[L];             // exp2(cum_last - cum_t): from token t to the tile's end
+  float into[L];             // tail dt: what the token's input weighs in the state behind the tile
+  float row[L];              // exp2(cum_t - cum before t's block)
+  float col[L / 16 - 1][L];  // [tb - 1][s], s before block tb: exp2(cum before tb - cum_s)
+  float fade;                // exp2(cum_last)
 
   // By one wave; lane = token, dt = 0 from the tile's valid tokens on.
   // Returns log2 of the whole tile's decay.
   __device__ __forceinline__ double fill(float step, float a, int lane) {
     constexpr double LOG2E = 1.4426950408889634074;
     const double cum = wave_scan(static_cast<double>(step) * (static_cast<double>(a) * LOG2E));
-    const double all = last_lane(cum);
+    const double all = lane_of(cum, 63);
+    double before = 0.0;     // cum before the lane's block
+#pragma unroll
+    for (int tb = 1; tb < L / 16; ++tb) {
+      const double start = lane_of(cum, 16 * tb - 1);
+      if (lane >= 16 * tb) before = start;
+      else col[tb - 1][lane] = exp2_raw(static_cast<float>(start - cum));
+    }
     if (lane < L) {
       const float h = static_cast<float>(cum);
       hi[lane] = h;
       lo[lane] = static_cast<float>(cum - static_cast<double>(h));
       dt[lane] = step;
       head[lane] = exp2_raw(h);
-      tail[lane] = exp2_raw(static_cast<float>(all - cum));
+      const float to_end = exp2_raw(static_cast<float>(all - cum));
+      tail[lane] = to_end;
+      into[lane] = to_end * step;
+      row[lane] = exp2_raw(static_cast<float>(cum - before));
     }
+    if (lane == 0) fade = exp2_raw(static_cast<float>(all));
     return all;
   }
-  // of tokens t .. t + 3: what the input of each weighs in the state behind
-  // the tile, and what the state in front of it weighs at each
-  __device__ __forceinline__ f32x4 into_state(int t) const {
-    return *reinterpret_cast<const f32x4*>(&tail[t]) * *reinterpret_cast<const f32x4*>(&dt[t]);
+  // exp of the decay exponents summed over tokens s+1 .. t for s = s0 .. s0 + 3
+  // and one t of block tb; 0 where s > t
+  __device__ __forceinline__ f32x4 fades(int tb, int t, int s0) const {
+    if (s0 < 16 * tb) return *reinterpret_cast<const f32x4*>(&col[tb - 1][s0]) * row[t];
+    const f32x4 h = *reinterpret_cast<const f32x4*>(&hi[s0]);
+    const f32x4 l = *reinterpret_cast<const f32x4*>(&lo[s0]);
+    f32x4 w;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const float e = exp2_raw((hi[t] - h[r]) + (lo[t] - l[r]));
+      w[r] = s0 + r <= t ? e : 0.f;
+    }
+    return w;
   }
-  __device__ __forceinline__ f32x4 from_state(int t) const {
-    return *reinterpret_cast<const f32x4*>(&head[t]);
-  }
-  // exp of the decay exponents summed over tokens s+1 .. t
-  __device__ __forceinline__ float fade(int t, int s) const {
-    return exp2_raw((hi[t] - hi[s]) + (lo[t] - lo[s]));
+  __device__ __forceinline__ f32x4 steps(int s0) const {
+    return *reinterpret_cast<const f32x4*>(&dt[s0]);
   }
 };
 
@@ -272,26 +340,66 @@ __device__ __forceinline__ const char* row_ptr(const void* p, size_t row, int wi
   return static_cast<const char*>(p) + row * width * (NI == 1 ? 2 : 4);
 }
 
-// S = fade S + B^T diag(w) X over a tile: rows n of S from A = B^T, the wave's
-// 16 features from the weighted X, in three parts.  weight(t) gives the
-// weights of tokens t .. t + 3.
-template <int NI, int L, int N, class Weight>
-__device__ __forceinline__ void add_tile(f32x4 (&S)[N / 16], const Plane<NI, L, N>& b,
-                                         const Plane<NI, L, SSM_P>& x, float fade, Weight weight,
-                                         int wave, int g, int c) {
+// Which unit and segment a workgroup works on (`count` segments per unit), as
+// scalars: the divisions run on vector registers.
+struct Place {
+  int seg, h;
+  size_t unit, shared;   // shared: the row of the head's group in b and c
+  __device__ __forceinline__ Place(const SsmArgs& a, uint32_t id, int count) {
+    const uint32_t u = __builtin_amdgcn_readfirstlane(id / count);
+    seg = id - u * count;
+    const uint32_t b = __builtin_amdgcn_readfirstlane(u / a.H);
+    h = u - b * a.H;
+    unit = u;
+    shared = static_cast<size_t>(b) * a.G +
+             __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(h) / (a.H / a.G));
+  }
+};
+
+// S = fade S + B^T diag(w) X over a tile, w by token: rows 16 i0 .. of S, COUNT
+// blocks of 16, from A = B^T, the features 16 pb .. of x from the weighted X,
+// in three parts.
+template <int COUNT, int NI, int L, int N>
+__device__ __forceinline__ void add_tile(f32x4 (&S)[COUNT], const Plane<NI, L, N>& b, int i0,
+                                         const Plane<NI, L, SSM_P>& x, int pb, float fade,
+                                         const float (&weight)[L], int g, int c) {
 #pragma unroll
-  for (int i = 0; i < N / 16; ++i) S[i] *= fade;
+  for (int i = 0; i < COUNT; ++i) S[i] *= fade;
 #pragma unroll
   for (int k = 0; k < L / 32; ++k) {
-    const Parts<NI> xs = x.cols(32 * k, 16 * wave, g, c);
+    const Parts<NI> xs = x.cols(32 * k, 16 * pb, g, c);
     f32x4 w[2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) w[h] = frag_half(xs, h) * weight(32 * k + 16 * h + 4 * g);
+    for (int h = 0; h < 2; ++h)
+      w[h] = frag_half(xs, h) *
+             *reinterpret_cast<const f32x4*>(&weight[32 * k + 16 * h + 4 * g]);
     const Parts<3> xw = split_frag<3>(w[0], w[1]);
 #pragma unroll
-    for (int i = 0; i < N / 16; ++i)
-      S[i] = mfma_parts(b.cols(32 * k, 16 * i, g, c), xw, S[i]);
+    for (int i = 0; i < COUNT; ++i)
+      S[i] = mfma_parts(b.cols(32 * k, 16 * (i0 + i), g, c), xw, S[i]);
   }
+}
+
+// The states of segments, each slot (`size` floats apart) holding what its
+// segment adds, become the states in front of them, starting from S;
+// `count` segments' additions are used and `slots` slots written.  dir = 1:
+// first segment to last, -1: last to first.  Returns the state behind.  The
+// loads of eight segments are issued together.
+__device__ __forceinline__ f32x4 join_segments(float* p, int64_t size, const double* fades,
+                                               int slots, int count, int dir, f32x4 S) {
+  for (int s0 = 0; s0 < slots; s0 += 8) {
+    f32x4 added[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (s0 + k < count) added[k] = *reinterpret_cast<const f32x4*>(p + dir * (s0 + k) * size);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int s = s0 + k;
+      if (s < slots) *reinterpret_cast<f32x4*>(p + dir * s * size) = S;
+      if (s < count) S = S * exp2_raw(static_cast<float>(fades[dir * s])) + added[k];
+    }
+  }
+  return S;
 }
 
 }  // namespace tttk
