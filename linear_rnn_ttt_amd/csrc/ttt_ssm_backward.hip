@@ -175,7 +175,7 @@ __global__ __launch_bounds__(GT, NI == 1 && N <= 64 ? 4 : 2) void ttt_ssm_bwd_k(
   constexpr int NB = N >= 64 ? N / 64 : 1;   // state row blocks of a wave (N = 32: waves 0, 1, 4, 5)
   __shared__ alignas(16) Lds lds;
   const SsmArgs& f = a.f;
-  const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, c = lane & 15;
+  const int tid = threadIdx.x, lane = tid & 63, g0 = lane >> 4, c0 = lane & 15;
   const int full_wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wave = full_wave & 3, half = full_wave >> 2;
   const Place at(f, blockIdx.x, f.segs);
@@ -196,12 +196,12 @@ __global__ __launch_bounds__(GT, NI == 1 && N <= 64 ? 4 : 2) void ttt_ssm_bwd_k(
     for (int i = 0; i < NA; ++i)
 #pragma unroll
       for (int r = 0; r < 4; ++r)
-        A[i][r] = from[(16 * (half * NA + i) + 4 * g + r) * P + 16 * wave + c];
+        A[i][r] = from[(16 * (half * NA + i) + 4 * g0 + r) * P + 16 * wave + c0];
   }
   // a state by rows: row 16 (wave + 4 nb) + c, features 32 k + 16 hh + 4 g .. of lane (g, c)
   auto row_of = [&](const float* p, int nb, int k, int hh) {
-    return *reinterpret_cast<const f32x4*>(p + (16 * (wave + 4 * nb) + c) * P + 32 * k + 16 * hh +
-                                           4 * g);
+    return *reinterpret_cast<const f32x4*>(p + (16 * (wave + 4 * nb) + c0) * P + 32 * k + 16 * hh +
+                                           4 * g0);
   };
   const float* seg_state = f.ws_state + (unit * f.segs + seg) * (N * P);
   double rest = f.ws_fade[unit * f.segs + seg];   // log2 decay from the segment's start
@@ -212,23 +212,23 @@ __global__ __launch_bounds__(GT, NI == 1 && N <= 64 ? 4 : 2) void ttt_ssm_bwd_k(
   Fetch<NI, L, N, GT> fb, fc;
   auto valid_of = [&](int tile) { return tile >= first ? min(L, f.T - tile * L) : 0; };
   auto fetch = [&](int tile) {
-    const int t0 = tile * L, valid = valid_of(tile);
-    fx.load(row_ptr<NI>(f.x, unit * f.T + t0, P), valid, tid);
-    fy.load(row_ptr<NI>(a.dy, unit * f.T + t0, P), valid, tid);
-    fb.load(row_ptr<NI>(f.b, shared * f.T + t0, N), valid, tid);
-    fc.load(row_ptr<NI>(f.c, shared * f.T + t0, N), valid, tid);
+    const int t0 = tile * L, valid = valid_of(tile), id = anew(tid);
+    fx.load(row_ptr<NI>(f.x, unit * f.T + t0, P), valid, id);
+    fy.load(row_ptr<NI>(a.dy, unit * f.T + t0, P), valid, id);
+    fb.load(row_ptr<NI>(f.b, shared * f.T + t0, N), valid, id);
+    fc.load(row_ptr<NI>(f.c, shared * f.T + t0, N), valid, id);
   };
   auto steps_of = [&](int tile) {
     return load_steps(f.dt + unit * f.T + tile * L, valid_of(tile), lane);
   };
-  // ddt of a tile whose sums stand in LDS, and its share of da; by one wave
-  auto finish = [&](int tile) {
+  // ddt of a tile whose sums stand in LDS, and its share of da; by one wave,
+  // which kept the tile's steps and its fade
+  auto finish = [&](int tile, float dt, float fade) {
     const int e = tile & 1, valid = valid_of(tile);
-    const Tokens<L>& tk = lds.tk[e];
+    const int lane = anew(tid & 63);
     double after = 0.0, upto = 0.0;   // of the token: u + row - column sums of Z; dt v
-    float dt = 0.f, direct = 0.f;
+    float direct = 0.f;
     if (lane < L) {
-      dt = tk.dt[lane];
       const float us = (lds.u[e][0][lane] + lds.u[e][1][lane]) +
                        (lds.u[e][2][lane] + lds.u[e][3][lane]);
       const float vs = (lds.v[e][0][lane] + lds.v[e][1][lane]) +
@@ -246,25 +246,21 @@ __global__ __launch_bounds__(GT, NI == 1 && N <= 64 ? 4 : 2) void ttt_ssm_bwd_k(
     }
     const double after_to = wave_scan(after), upto_to = wave_scan(upto);
     const float d = (lds.dot[e][0] + lds.dot[e][1]) + (lds.dot[e][2] + lds.dot[e][3]);
-    const double ex = (last_lane(after_to) - after_to + after) + (upto_to - upto) + tk.fade * d;
+    const double ex = (last_lane(after_to) - after_to + after) + (upto_to - upto) + fade * d;
     if (lane < valid) {
       a.ddt[unit * f.T + tile * L + lane] = static_cast<float>(direct + ah * ex);
       da_sum += dt * ex;
     }
   };
 
-  fetch(end - 1);
-  float step = steps_of(end - 1);
-  if (full_wave == 7) {
-    rest -= lds.tk[(end - 1) & 1].fill(step, ah, lane);
-    if (lane == 0) lds.before = exp2_raw(static_cast<float>(rest));
-  }
-  step = steps_of(end - 2);
-  for (int tile = end - 1; tile >= first; --tile) {
-    const int t0 = tile * L, valid = valid_of(tile), e = tile & 1;
-    const Tokens<L>& tk = lds.tk[e];
-    // the segment's own part of the state before the tile
-    f32x4 own[NB][P / 32][2];
+  // the segment's own part of the state before a tile
+  f32x4 own[NB][P / 32][2];
+  auto load_own = [&](int tile) {
+    const int g0 = anew((tid & 63) >> 4), c0 = anew(tid & 15);
+    auto row_of = [&](const float* p, int nb, int k, int hh) {
+      return *reinterpret_cast<const f32x4*>(p + (16 * (wave + 4 * nb) + c0) * P + 32 * k +
+                                             16 * hh + 4 * g0);
+    };
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -274,10 +270,25 @@ __global__ __launch_bounds__(GT, NI == 1 && N <= 64 ? 4 : 2) void ttt_ssm_bwd_k(
           own[nb][k][hh] = has_rows && tile > first
                                ? row_of(a.ws_tile + (unit * tiles + tile) * (N * P), nb, k, hh)
                                : zero;
-    fx.store(lds.x, tid);
-    fy.store(lds.dy, tid);
-    fb.store(lds.b, tid);
-    fc.store(lds.c, tid);
+  };
+  fetch(end - 1);
+  load_own(end - 1);
+  float step = steps_of(end - 1);
+  if (full_wave == 7) {
+    rest -= lds.tk[(end - 1) & 1].fill(step, ah, lane);
+    if (lane == 0) lds.before = exp2_raw(static_cast<float>(rest));
+  }
+  step = steps_of(end - 2);
+  float done_dt = 0.f, done_fade = 0.f;   // of the tile to finish
+  for (int tile = end - 1; tile >= first; --tile) {
+    const int t0 = tile * L, valid = valid_of(tile), e = tile & 1;
+    const Tokens<L>& tk = lds.tk[e];
+    int g = anew(g0), c = anew(c0);
+    const int id = anew(tid);
+    fx.store(lds.x, id);
+    fy.store(lds.dy, id);
+    fb.store(lds.b, id);
+    fc.store(lds.c, id);
 #pragma unroll
     for (int i = 0; i < NA; ++i) {
       u32x2 p[3];
@@ -288,9 +299,9 @@ __global__ __launch_bounds__(GT, NI == 1 && N <= 64 ? 4 : 2) void ttt_ssm_bwd_k(
     }
     lds_barrier();
     const float before = lds.before;
-    fetch(tile - 1);
 
     // what the adjoint behind the tile and the state before it give
+    g = anew(g0), c = anew(c0);
     f32x4 dx[JN], db[NB][JN], dc[NB][JN];
 #pragma unroll
     for (int jj = 0; jj < JN; ++jj) {
@@ -362,15 +373,12 @@ __global__ __launch_bounds__(GT, NI == 1 && N <= 64 ? 4 : 2) void ttt_ssm_bwd_k(
         lds.v[e][wave][t] = vs;
       }
     }
-    if (full_wave == 7) {   // the tile behind is done, the one before is next
-      if (tile < end - 1) finish(tile + 1);
-      if (tile > first) rest -= lds.tk[e ^ 1].fill(step, ah, lane);
-    }
-    step = steps_of(tile - 2);
     lds_barrier();
-    if (full_wave == 7 && lane == 0) lds.before = exp2_raw(static_cast<float>(rest));
+    fetch(tile - 1);
+    load_own(tile - 1);
 
     // W1 and W2 block by block
+    g = anew(g0), c = anew(c0);
     for (int i = full_wave; i < Lds::BLOCKS; i += GT / 64) {
       int tb, sb;
       block_of(i, &tb, &sb);
@@ -421,9 +429,21 @@ __global__ __launch_bounds__(GT, NI == 1 && N <= 64 ? 4 : 2) void ttt_ssm_bwd_k(
         lds.w2.put4(k, t, s0, u32x2{0u, 0u});
       }
     }
+    // by waves with one block: the tile behind is finished, the one before prepared
+    if (full_wave == 6) {
+      if (tile < end - 1) finish(tile + 1, done_dt, done_fade);
+      done_dt = lane < L ? tk.dt[lane] : 0.f;
+      done_fade = tk.fade;
+    }
+    if (full_wave == 7 && tile > first) {
+      rest -= lds.tk[e ^ 1].fill(step, ah, lane);
+      if (lane == 0) lds.before = exp2_raw(static_cast<float>(rest));
+    }
+    step = steps_of(tile - 2);
     lds_barrier();
 
     // and the tile's own tokens
+    g = anew(g0), c = anew(c0);
 #pragma unroll
     for (int k = 0; k < L / 32; ++k) {
       const Parts<NI> yt = lds.dy.cols(32 * k, 16 * wave, g, c);
@@ -485,23 +505,24 @@ __global__ __launch_bounds__(GT, NI == 1 && N <= 64 ? 4 : 2) void ttt_ssm_bwd_k(
     }
 
     // A before the tile
+    g = anew(g0), c = anew(c0);
     add_tile(A, lds.c, half * NA, lds.dy, wave, tk.fade, tk.head, g, c);
     lds_barrier();
   }
-  if (full_wave == 7) finish(first);
+  if (full_wave == 6) finish(first, done_dt, done_fade);
   if (a.dstate0 && seg == 0) {
     float* out = a.dstate0 + unit * (N * P);
 #pragma unroll
     for (int i = 0; i < NA; ++i)
 #pragma unroll
       for (int r = 0; r < 4; ++r)
-        out[(16 * (half * NA + i) + 4 * g + r) * P + 16 * wave + c] = A[i][r];
+        out[(16 * (half * NA + i) + 4 * g0 + r) * P + 16 * wave + c0] = A[i][r];
   }
   // the segment's da and dd
   dd_sum = wave_sum(dd_sum);
   if (lane == 0) lds.dd[full_wave] = dd_sum;
   lds_barrier();
-  if (full_wave == 7) {
+  if (full_wave == 6) {
     const double all = last_lane(wave_scan(da_sum));
     if (lane == 0) {
       float* out = a.ws_sums + (unit * f.segs + seg) * 2;

@@ -340,6 +340,13 @@ __device__ __forceinline__ const char* row_ptr(const void* p, size_t row, int wi
   return static_cast<const char*>(p) + row * width * (NI == 1 ? 2 : 4);
 }
 
+// A lane index that the compiler takes for a new value: LDS addresses made from
+// it are made where they are used and not kept in registers around the loop.
+__device__ __forceinline__ int anew(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
 // Which unit and segment a workgroup works on (`count` segments per unit), as
 // scalars: the divisions run on vector registers.
 struct Place {
