@@ -105,6 +105,19 @@ __device__ __forceinline__ float row_sum16(float x) {
   return x;
 }
 
+// The sums of four values over the 16 lanes of a row, lane c holding that of
+// x[c % 4]: neighbours exchange what the other is to sum, then lanes 4 and 8
+// apart are added (half the instructions of four whole sums).
+__device__ __forceinline__ float row_sums4(f32x4 x, int c) {
+  const bool odd = c & 1, high = c & 2;
+  const float a = (odd ? x[1] : x[0]) + row_peer<0xb1>(odd ? x[0] : x[1]);
+  const float b = (odd ? x[3] : x[2]) + row_peer<0xb1>(odd ? x[2] : x[3]);
+  float s = (high ? b : a) + row_peer<0x4e>(high ? a : b);
+  s += row_peer<0x124>(s);   // row_ror 4
+  s += row_peer<0x128>(s);   // row_ror 8
+  return s;
+}
+
 // Sum over the 64 lanes, in every lane.
 __device__ __forceinline__ float wave_sum(float x) { return group_sum(row_sum16(x)); }
 

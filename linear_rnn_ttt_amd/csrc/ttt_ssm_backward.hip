@@ -316,7 +316,7 @@ __global__ __launch_bounds__(GT, NI == 1 && N <= 64 ? 4 : 2) void ttt_ssm_bwd_k(
       for (int jj = 0; jj < JN; ++jj)
         dx[jj] = mfma_parts(ap, lds.b.rows(16 * block(jj), 32 * k, g, c), dx[jj]);
     }
-    float dot = 0.f;
+    f32x4 sa = zero;   // S A^T of the wave's rows: <S, A> on its diagonal
     if (has_rows) {
 #pragma unroll
       for (int k = 0; k < P / 32; ++k) {
@@ -330,14 +330,9 @@ __global__ __launch_bounds__(GT, NI == 1 && N <= 64 ? 4 : 2) void ttt_ssm_bwd_k(
             db[nb][jj] =
                 mfma_parts(ar, lds.x.rows(16 * block(jj), 32 * k, g, c), db[nb][jj]);
 #pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            S[hh] = S[hh] * before + own[nb][k][hh];
-            if (half == 0) {
-              const f32x4 prod = frag_half(ar, hh) * S[hh];
-              dot += (prod[0] + prod[1]) + (prod[2] + prod[3]);
-            }
-          }
+          for (int hh = 0; hh < 2; ++hh) S[hh] = S[hh] * before + own[nb][k][hh];
           const Parts<3> sp = split_frag<3>(S[0], S[1]);
+          if (half == 0) sa = mfma_parts(sp, ar, sa);
 #pragma unroll
           for (int jj = 0; jj < JN; ++jj)
             dc[nb][jj] =
@@ -346,6 +341,9 @@ __global__ __launch_bounds__(GT, NI == 1 && N <= 64 ? 4 : 2) void ttt_ssm_bwd_k(
       }
     }
     if (half == 0) {
+      float dot = 0.f;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) dot += 4 * g + r == c ? sa[r] : 0.f;
       dot = wave_sum(dot);
       if (lane == 0) lds.dot[e][wave] = dot;
     }
@@ -396,6 +394,7 @@ __global__ __launch_bounds__(GT, NI == 1 && N <= 64 ? 4 : 2) void ttt_ssm_bwd_k(
       const f32x4 z = gt * xt * fade;
       f32x4 w1 = gt * (fade * dt), w2 = xt * (fade * dt);
       float row = 0.f;
+      f32x4 off;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const bool diagonal = tb == sb && 4 * g + r == c;
@@ -404,11 +403,11 @@ __global__ __launch_bounds__(GT, NI == 1 && N <= 64 ? 4 : 2) void ttt_ssm_bwd_k(
           dd_sum += xt[r];
           w1[r] += skip;
         }
-        const float off = diagonal ? 0.f : z[r];
-        row += off * dt[r];
-        const float col = row_sum16(off);
-        if (c == r) lds.zcol[e][i][4 * g + r] = col;
+        off[r] = diagonal ? 0.f : z[r];
+        row += off[r] * dt[r];
       }
+      const float col = row_sums4(off, c);
+      if (c < 4) lds.zcol[e][i][4 * g + c] = col;
       row = group_sum(row);
       if (g == 0) lds.zrow[e][i][c] = row;
       u32x2 p[NM], q[NM];
