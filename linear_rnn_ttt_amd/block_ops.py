@@ -84,6 +84,10 @@ def _on_stream(func):
     def call(*args, stream=None, **kw):
         if stream is None:
             return func(*args, **kw)
+        data = args[0] if args else kw.get("x", kw.get("r"))
+        if isinstance(data, torch.Tensor) and data.device != stream.device:
+            raise ValueError("stream must be on %s, like the data (got %s)"
+                             % (data.device, stream.device))
         with torch.cuda.stream(stream):
             return func(*args, **kw)
     return call
