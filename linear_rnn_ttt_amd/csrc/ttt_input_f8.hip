@@ -5,14 +5,20 @@
 // and its outputs: q, k, v bf16 in [B, H, T, 64] and eta = eta_base /
 // (1 + exp(-(y + b_eta))) fp32.
 //
-// Tiling: BM x BN outputs per workgroup, 64 columns (one head, or gates) and
-// BM / WM rows per wave.  D is walked in steps of 128 bytes through two LDS
-// buffers, the next step's copies (global_load_lds) on their way while one is
-// worked on; the 16-byte chunk q of row r sits at chunk q ^ (r % 8).  One
-// 16x16x128 product takes chunks g and g + 4 of its rows (the same for both
-// operands, so the contraction's order does not matter).  D is a multiple of
-// 64: an odd last half step fetches its first half twice and multiplies the
-// second copy by zero.
+// Tiling: D is walked in steps of 128 bytes through two LDS buffers, the next
+// step's copies (global_load_lds) on their way while one is worked on.  The
+// 16-byte chunks of a row are swizzled so that a fragment's rows spread over the
+// banks.  One 16x16x128 product takes chunks g and g + 4 of its rows (the same
+// for both operands, so the contraction's order does not matter).  D is a
+// multiple of 64: an odd last half step fetches its first half twice and
+// multiplies the second copy by zero.  With enough tiles for every compute unit
+// a workgroup takes 256 x 256 outputs at a time (f8_stream), else 128 x 128
+// (f8_tile): at 2300 x 7680 outputs the larger are 270 tiles.
+//
+// What bounds it (B4 T8192 D2048 H32, 396 us, 2.1 PFLOP/s; a library product of
+// this size reaches 3.0): the products alone take 288 us of every 2048 of D,
+// where reads, products and barriers of the two groups of waves alternate, and
+// the 403 MB of outputs some 70 us beside them.
 //
 // The same columns come a second way, f8_block: 64 x 32 outputs per workgroup,
 // each wave a share of D read from memory straight into fragments, the waves'
@@ -26,9 +32,11 @@
 // that of an fp32 gate: gates are summed by 16x16x32 bf16 products (widening
 // e4m3 to bf16 is exact), whose sums are fp32.  They have workgroups of their
 // own, the launch's first: 1 column in 193, and a branch for them inside the
-// tile's loop cost its schedule (527 -> XXX us at B4 T8192 D2048 H32).
+// tile's loop spoils its schedule (594 -> 432 us at B4 T8192 D2048 H32 with
+// 256 x 256 tiles).  They take no measurable time there.
 //
-// Tile order over the 8 XCDs as in ttt_input.hip.
+// Tile order: each of the 8 XCDs (consecutive workgroups land on them in turn)
+// takes a contiguous run of tiles.
 #include <type_traits>
 
 #include "ttt_block.hpp"
@@ -174,64 +182,21 @@ __device__ __forceinline__ void f8_tile(const InputF8Args& a, F8Tile<WM, WN, MI>
       for (int j = 0; j < 4; ++j) acc[i][j] = mfma_f8(a0[i], a1[i], b0[j], b1[j], acc[i][j]);
   };
   auto landed = [] { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); };
-  // a barrier that products do not cross either
-  auto meet = [] {
-    __builtin_amdgcn_sched_barrier(0);
-    lds_barrier_copies_in_flight();
-    __builtin_amdgcn_sched_barrier(0);
-  };
-  if constexpr (WM * WN == 8) {
-    // Two waves per SIMD, waves w and w + 4, half a step apart: while one
-    // group reads its fragments, the other's products run.  With phases
-    // between barriers, the first group reads step s in phase 2 s and
-    // multiplies in 2 s + 1, the second a phase later; step s + 2 may replace
-    // s in its buffer from phase 2 s + 2 on, and has to have landed by the
-    // end of 2 s + 3.
-    const bool second = wave >= 4;
-    issue(0);
-    if (steps > 1) {
-      issue(1);
-      asm volatile("s_waitcnt vmcnt(%0)" ::"n"(CA + CB) : "memory");
-    } else {
-      landed();
-    }
-    meet();
-    auto step = [&](int s, auto whole) {
-      if (!second && s > 0 && s + 1 < steps) issue(s + 1);
-      read(s & 1, whole);
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-      if (second) landed();
-      meet();
-      if (second && s + 2 < steps) issue(s + 2);
-      __builtin_amdgcn_s_setprio(1);
-      multiply();
-      __builtin_amdgcn_s_setprio(0);
-      __builtin_amdgcn_sched_barrier(0);
-      if (!second) landed();
-      meet();
-    };
-    if (second) meet();
-    const int whole = odd ? steps - 1 : steps;
-    for (int s = 0; s < whole; ++s) step(s, std::true_type{});
-    if (odd) step(whole, std::false_type{});
-    if (!second) meet();
-  } else {
-    // One wave per SIMD and two workgroups per compute unit: the other
-    // workgroup's products run beside this one's reads.
-    auto step = [&](int s, auto whole) {
-      if (s + 1 < steps) issue(s + 1);
-      read(s & 1, whole);
-      multiply();
-      landed();
-      lds_barrier_copies_in_flight();
-    };
-    issue(0);
+  // One wave per SIMD and two workgroups per compute unit: the other
+  // workgroup's products run beside this one's reads.
+  auto step = [&](int s, auto whole) {
+    if (s + 1 < steps) issue(s + 1);
+    read(s & 1, whole);
+    multiply();
     landed();
     lds_barrier_copies_in_flight();
-    const int whole = odd ? steps - 1 : steps;
-    for (int s = 0; s < whole; ++s) step(s, std::true_type{});
-    if (odd) step(whole, std::false_type{});
-  }
+  };
+  issue(0);
+  landed();
+  lds_barrier_copies_in_flight();
+  const int whole = odd ? steps - 1 : steps;
+  for (int s = 0; s < whole; ++s) step(s, std::true_type{});
+  if (odd) step(whole, std::false_type{});
 
   // epilogue: accumulator (i, j) holds row m0 + 16 (MI wm + i) + 4 g + r, column nb0 + 16 j + c
   const int T = a.T, H = a.H;
@@ -273,6 +238,228 @@ __device__ __forceinline__ void f8_tile(const InputF8Args& a, F8Tile<WM, WN, MI>
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // read before the next part's writes
   }
+}
+
+// Many rows: a workgroup per compute unit takes 256 x 256 tiles one after
+// another, eight waves of 128 rows x 64 columns (one head), and its stream of
+// steps runs on across tiles, so that a tile's first steps land while the last
+// one's products and stores are under way.
+//
+// The products are W_in x^T: with rows 32 (i / 2) + 8 (c / 4) + 4 (i % 2) + c % 4
+// of the head in block i, a lane holds features 8 g .. 8 g + 7 and 32 + 8 g .. of
+// one token, and its two stores of 16 bytes fill half a 128-byte row each with
+// those of three other lanes.
+struct F8Stream {
+  static constexpr int BM = 256, BN = 256, NT = 512, GRID = 256;
+  uint8_t a[2][BM][BK];
+  uint8_t b[2][BN][BK];
+  // scales of the workgroup's last tiles: with one step a tile, the second
+  // tile behind one is fetched while the first is being stored
+  float sx[4][BM], sw[4][BN];
+};
+
+__device__ __forceinline__ void f8_stream(const InputF8Args& a, F8Stream& L, int id) {
+  constexpr int BM = F8Stream::BM, BN = F8Stream::BN, MI = 8;
+  const int M = a.B * a.T, N = 3 * a.H * HD, D = a.D;   // without the gates
+  const int ntm = (M + BM - 1) / BM, ntn = (N + BN - 1) / BN, nt = ntm * ntn;
+  // groups of as many columns of tiles as have 3 MB of weights, which stay in an
+  // XCD's L2 while the rows of x pass by
+  const int cols = max(1, (3 << 20) / (BN * D));
+  // each XCD a contiguous run of tiles, its 32 workgroups taking them in turn
+  const int per = (nt + XCDS - 1) / XCDS, run = (id % XCDS) * per;
+  const int run_end = min(run + per, nt), stride = F8Stream::GRID / XCDS;
+  const int first = run + id / XCDS;
+  if (first >= run_end) return;
+  const int steps = (D + BK - 1) / BK;
+  const bool odd = D % BK != 0;
+  const int total = ((run_end - first - 1) / stride + 1) * steps;
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int g = lane >> 4, c = lane & 15, wm = wave >> 2, wn = wave & 3;
+  const bool second = wm == 1;
+  auto rows_at = [&](int tile, int* m0, int* n0) {
+    const int grp = tile / (cols * ntm), within = tile - grp * (cols * ntm);
+    const int gsize = min(cols, ntn - grp * cols);
+    const int row = within / gsize;
+    *m0 = __builtin_amdgcn_readfirstlane(row * BM);
+    *n0 = __builtin_amdgcn_readfirstlane((grp * cols + within - row * gsize) * BN);
+  };
+
+  // copies: 8 rows of 128 bytes per wave instruction, lane l landing at byte
+  // 16 l, i.e. in slot cq of row cr, which holds chunk cq ^ (the row's swizzle):
+  // r % 8 for x, and for W_in r % 4 + 4 (r / 8 % 2), as its fragments' rows run
+  const int cr = lane >> 3, cq = lane & 7;
+  const int qa = cq ^ cr, qb = cq ^ ((cr & 3) | (wave & 1) << 2);
+  const uint8_t *xg = nullptr, *wg = nullptr;
+  int last_x = 0, last_w = 0;   // rows of the tile that exist, less one
+  int next_tile = first, next_step = 0, issued = 0;
+  auto row_of = [&](int j, int last) {
+    return static_cast<uint32_t>(min(8 * (wave + 8 * j) + cr, last)) * static_cast<uint32_t>(D);
+  };
+  auto issue = [&] {
+    if (next_step == 0) {   // a new tile: its rows (clamped at the ends) and scales
+      int m0, n0;
+      rows_at(next_tile, &m0, &n0);
+      xg = static_cast<const uint8_t*>(a.x) + static_cast<size_t>(m0) * D;
+      wg = static_cast<const uint8_t*>(a.w) + static_cast<size_t>(n0) * D;
+      last_x = M - 1 - m0;
+      last_w = N - 1 - n0;
+      const int buf = ((next_tile - first) / stride) & 3;
+      const float* from = wm == 0 ? a.x_scale + min(m0 + 64 * wn + lane, M - 1)
+                                  : a.w_scale + min(n0 + 64 * wn + lane, N - 1);
+      float* to = wm == 0 ? &L.sx[buf][64 * wn] : &L.sw[buf][64 * wn];
+      __builtin_amdgcn_global_load_lds(from, (TTT_LDS void*)to, 4, 0, 0);
+    }
+    const bool short_step = odd && next_step == steps - 1;   // chunks 4-7 lie past the row's end
+    const uint32_t at = next_step * BK;
+    const uint32_t ka = at + 16 * (short_step ? qa & 3 : qa);
+    const uint32_t kb = at + 16 * (short_step ? qb & 3 : qb);
+    const int buf = issued & 1;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      __builtin_amdgcn_global_load_lds(xg + (row_of(j, last_x) + ka),
+                                       (TTT_LDS void*)&L.a[buf][8 * (wave + 8 * j)][0], 16, 0, 0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      __builtin_amdgcn_global_load_lds(wg + (row_of(j, last_w) + kb),
+                                       (TTT_LDS void*)&L.b[buf][8 * (wave + 8 * j)][0], 16, 0, 0);
+    ++issued;
+    if (++next_step == steps) {
+      next_step = 0;
+      next_tile += stride;
+    }
+  };
+
+  f32x4 acc[4][MI];
+  auto clear = [&] {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < MI; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  };
+  u32x4 x0[MI], x1[MI], w0[4], w1[4];
+  auto read = [&](int buf) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = 64 * wn + 32 * (i >> 1) + 8 * (c >> 2) + 4 * (i & 1) + (c & 3);
+      const int sw = (c & 3) | (((c >> 2) & 1) << 2);
+      w0[i] = *reinterpret_cast<const u32x4*>(&L.b[buf][r][(g ^ sw) << 4]);
+      w1[i] = *reinterpret_cast<const u32x4*>(&L.b[buf][r][((g + 4) ^ sw) << 4]);
+    }
+#pragma unroll
+    for (int j = 0; j < MI; ++j) {
+      const uint8_t* row = L.a[buf][128 * wm + 16 * j + c];
+      x0[j] = chunk(row, g, c);
+      x1[j] = chunk(row, g + 4, c);
+    }
+  };
+  auto drop_second_half = [&] {
+    const u32x4 zero = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w1[i] = zero;
+#pragma unroll
+    for (int j = 0; j < MI; ++j) x1[j] = zero;
+  };
+  auto store_tile = [&](int tile) {   // whether it made exactly 2 MI stores
+    int m0, n0;
+    rows_at(tile, &m0, &n0);
+    const int buf = ((tile - first) / stride) & 3, nb0 = n0 + 64 * wn;
+    if (nb0 >= N) return false;
+    f32x4 sw[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      sw[i] = *reinterpret_cast<const f32x4*>(
+          &L.sw[buf][64 * wn + 32 * (i >> 1) + 8 * g + 4 * (i & 1)]);
+    int h;
+    uint16_t* out = head_out(a, nb0, &h);
+    const uint32_t T = a.T;
+    auto put = [&](int j, auto whole) {
+      const uint32_t in = 128 * wm + 16 * j + c, m = m0 + in;
+      const float sx = L.sx[buf][in];
+      const uint32_t b = m / T, t = m - b * T;
+      uint16_t* p = out + ((static_cast<size_t>(b) * a.H + h) * T + t) * HD + 8 * g;
+      u32x4 v[2];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const f32x4 y = acc[i][j] * (sw[i] * sx);
+        v[i >> 1][2 * (i & 1)] = pack_bf16(y[0], y[1]);
+        v[i >> 1][2 * (i & 1) + 1] = pack_bf16(y[2], y[3]);
+      }
+      if (whole || m < static_cast<uint32_t>(M)) {
+        // past the L2, which holds what the products read (411 -> 396 us)
+        __builtin_nontemporal_store(v[0], reinterpret_cast<u32x4*>(p));
+        __builtin_nontemporal_store(v[1], reinterpret_cast<u32x4*>(p + 32));
+      }
+    };
+    if (m0 + BM <= M) {
+#pragma unroll
+      for (int j = 0; j < MI; ++j) put(j, std::true_type{});
+      return true;
+    }
+#pragma unroll
+    for (int j = 0; j < MI; ++j) put(j, std::false_type{});
+    return false;
+  };
+  // The wave's copies have landed.  Stores are counted with them, in the order
+  // of issue: where exactly the 16 of a whole tile follow the copies, they are
+  // left under way.
+  auto landed = [](bool stores) {
+    if (stores) asm volatile("s_waitcnt vmcnt(16)" ::: "memory");
+    else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  };
+  // a barrier that products do not cross either
+  auto meet = [] {
+    __builtin_amdgcn_sched_barrier(0);
+    lds_barrier_copies_in_flight();
+    __builtin_amdgcn_sched_barrier(0);
+  };
+
+  // Two waves per SIMD, w and w + 4, half a step apart: while one group reads
+  // its fragments, the other's products run.  With phases between barriers,
+  // the first group reads step s in phase 2 s and multiplies in 2 s + 1, the
+  // second a phase later; step s + 2 may replace s in its buffer from phase
+  // 2 s + 2 on, and has to have landed by the end of 2 s + 3.
+  clear();
+  issue();
+  if (total > 1) issue();
+  landed(false);
+  meet();
+  if (second) meet();
+  int tile = first, in_tile = 0;
+  bool stores = false;   // behind the last copies
+  for (int s = 0; s < total; ++s) {
+    if (!second) {
+      if (s > 0 && s + 1 < total) issue();
+      stores = false;
+    }
+    read(s & 1);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    if (second) landed(stores);
+    meet();
+    if (second) {
+      if (s + 2 < total) issue();
+      stores = false;
+    }
+    const bool last = ++in_tile == steps;
+    if (odd && last) drop_second_half();
+    __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+    for (int j = 0; j < MI; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[i][j] = mfma_f8(w0[i], w1[i], x0[j], x1[j], acc[i][j]);
+    __builtin_amdgcn_s_setprio(0);
+    __builtin_amdgcn_sched_barrier(0);
+    if (last) {
+      stores = store_tile(tile);
+      clear();
+      in_tile = 0;
+      tile += stride;
+    }
+    if (!second) landed(stores);
+    meet();
+  }
+  if (!second) meet();
 }
 
 // 64 x 32 outputs, wave w of W taking steps w, w + W, ... of D.  GATE: the
@@ -363,20 +550,37 @@ __host__ __device__ inline int gate_blocks(int rows, int H) {
 
 // The bodies are device functions: the host pass leaves a kernel template that
 // holds the 16-byte global_load_lds without its launch stub.
-template <int WM, int WN, int MI>
-__global__ __launch_bounds__(WM * WN * 64) void ttt_input_f8_k(InputF8Args a) {
-  constexpr int W = WM * WN;
-  constexpr size_t bytes = sizeof(F8Tile<WM, WN, MI>) > sizeof(F8Part<W>)
-                               ? sizeof(F8Tile<WM, WN, MI>) : sizeof(F8Part<W>);
-  __shared__ alignas(16) char smem[bytes];
-  const int gates = (gate_blocks(a.B * a.T, a.H) + XCDS - 1) / XCDS * XCDS;
-  const int id = blockIdx.x;
-  if (id >= gates) {
-    f8_tile<WM, WN, MI>(a, *reinterpret_cast<F8Tile<WM, WN, MI>*>(smem), id - gates);
-  } else if (id < gate_blocks(a.B * a.T, a.H)) {
-    const int cols = (a.H + FN - 1) / FN;
-    f8_block<W, true>(a, *reinterpret_cast<F8Part<W>*>(smem), id / cols * FM, id % cols * FN);
+template <int W>
+__device__ __forceinline__ bool gate_role(const InputF8Args& a, char* smem, int* id) {
+  const int blocks = gate_blocks(a.B * a.T, a.H);
+  const int gates = (blocks + XCDS - 1) / XCDS * XCDS;
+  if (*id >= gates) {
+    *id -= gates;
+    return false;
   }
+  if (*id < blocks) {
+    const int cols = (a.H + FN - 1) / FN;
+    f8_block<W, true>(a, *reinterpret_cast<F8Part<W>*>(smem), *id / cols * FM, *id % cols * FN);
+  }
+  return true;
+}
+
+__global__ __launch_bounds__(F8Stream::NT) void ttt_input_f8_k(InputF8Args a) {
+  static_assert(sizeof(F8Stream) >= sizeof(F8Part<8>), "the gates' sums fit");
+  __shared__ alignas(16) char smem[sizeof(F8Stream)];
+  int id = blockIdx.x;
+  if (!gate_role<8>(a, smem, &id))
+    f8_stream(a, *reinterpret_cast<F8Stream*>(smem), id);
+}
+
+using F8Mid = F8Tile<2, 2, 4>;
+
+__global__ __launch_bounds__(F8Mid::NT) void ttt_input_f8_mid_k(InputF8Args a) {
+  static_assert(sizeof(F8Mid) >= sizeof(F8Part<4>), "the gates' sums fit");
+  __shared__ alignas(16) char smem[sizeof(F8Mid)];
+  int id = blockIdx.x;
+  if (!gate_role<4>(a, smem, &id))
+    f8_tile<2, 2, 4>(a, *reinterpret_cast<F8Mid*>(smem), id);
 }
 
 __global__ __launch_bounds__(512) void ttt_input_f8_few_k(InputF8Args a) {
@@ -391,30 +595,25 @@ __global__ __launch_bounds__(512) void ttt_input_f8_few_k(InputF8Args a) {
   }
 }
 
-template <int WM, int WN, int MI>
-hipError_t tile_launch(const InputF8Args& a, hipStream_t stream) {
-  using Tile = F8Tile<WM, WN, MI>;
-  const int64_t M = static_cast<int64_t>(a.B) * a.T, N = 3 * static_cast<int64_t>(a.H) * HD;
-  const int64_t nt = ((M + Tile::BM - 1) / Tile::BM) * ((N + Tile::BN - 1) / Tile::BN);
-  const int64_t gates = gate_blocks(static_cast<int>(M), a.H);
-  const int64_t blocks = (gates + XCDS - 1) / XCDS * XCDS + (nt + XCDS - 1) / XCDS * XCDS;
-  hipLaunchKernelGGL((ttt_input_f8_k<WM, WN, MI>), dim3(static_cast<uint32_t>(blocks)),
-                     dim3(Tile::NT), 0, stream, a);
-  return hipGetLastError();
-}
-
 }  // namespace
 
 hipError_t launch_input_f8(const InputF8Args& a, hipStream_t stream) {
   const int64_t M = static_cast<int64_t>(a.B) * a.T, N = 3 * static_cast<int64_t>(a.H) * HD;
+  auto tiles = [&](int64_t bm, int64_t bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
+  const int64_t gates = gate_blocks(static_cast<int>(M), a.H);
+  const int64_t padded = (gates + XCDS - 1) / XCDS * XCDS;
   if (M <= 128) {
-    const int64_t blocks = gate_blocks(static_cast<int>(M), a.H) + ((M + FM - 1) / FM) * (N / FN);
-    hipLaunchKernelGGL(ttt_input_f8_few_k, dim3(static_cast<uint32_t>(blocks)), dim3(512), 0,
-                       stream, a);
-    return hipGetLastError();
+    hipLaunchKernelGGL(ttt_input_f8_few_k, dim3(static_cast<uint32_t>(gates + tiles(FM, FN))),
+                       dim3(512), 0, stream, a);
+  } else if (tiles(256, 256) >= F8Stream::GRID) {
+    hipLaunchKernelGGL(ttt_input_f8_k, dim3(static_cast<uint32_t>(padded + F8Stream::GRID)),
+                       dim3(F8Stream::NT), 0, stream, a);
+  } else {
+    const int64_t nt = (tiles(F8Mid::BM, F8Mid::BN) + XCDS - 1) / XCDS * XCDS;
+    hipLaunchKernelGGL(ttt_input_f8_mid_k, dim3(static_cast<uint32_t>(padded + nt)),
+                       dim3(F8Mid::NT), 0, stream, a);
   }
-  if (((M + 255) / 256) * ((N + 255) / 256) >= 256) return tile_launch<2, 4, 8>(a, stream);
-  return tile_launch<2, 2, 4>(a, stream);
+  return hipGetLastError();
 }
 
 }  // namespace tttk
