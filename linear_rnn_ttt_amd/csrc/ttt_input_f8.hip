@@ -11,9 +11,9 @@
 // banks.  One 16x16x128 product takes chunks g and g + 4 of its rows (the same
 // for both operands, so the contraction's order does not matter).  D is a
 // multiple of 64: an odd last half step fetches its first half twice and
-// multiplies the second copy by zero.  With enough tiles for every compute unit
-// a workgroup takes 256 x 256 outputs at a time (f8_stream), else 128 x 128
-// (f8_tile): at 2300 x 7680 outputs the larger are 270 tiles.
+// multiplies the second copy by zero.  With tiles for most compute units a
+// workgroup takes 256 x 256 outputs at a time (f8_stream), else 128 x 128
+// (f8_tile).
 //
 // What bounds it (B4 T8192 D2048 H32, 396 us, 2.1 PFLOP/s; a library product of
 // this size reaches 3.0): the products alone take 288 us of every 2048 of D,
@@ -49,7 +49,7 @@ namespace {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
-constexpr int BK = 128, HD = 64, XCDS = 8, GM = 4;
+constexpr int BK = 128, HD = 64, XCDS = 8, CUS = 256, GM = 4;
 
 __device__ __forceinline__ float sigmoid(float y) { return 1.0f / (1.0f + expf(-y)); }
 
@@ -250,7 +250,7 @@ __device__ __forceinline__ void f8_tile(const InputF8Args& a, F8Tile<WM, WN, MI>
 // one token, and its two stores of 16 bytes fill half a 128-byte row each with
 // those of three other lanes.
 struct F8Stream {
-  static constexpr int BM = 256, BN = 256, NT = 512, GRID = 256;
+  static constexpr int BM = 256, BN = 256, NT = 512, GRID = CUS;
   uint8_t a[2][BM][BK];
   uint8_t b[2][BN][BK];
   // scales of the workgroup's last tiles: with one step a tile, the second
@@ -602,10 +602,18 @@ hipError_t launch_input_f8(const InputF8Args& a, hipStream_t stream) {
   auto tiles = [&](int64_t bm, int64_t bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
   const int64_t gates = gate_blocks(static_cast<int>(M), a.H);
   const int64_t padded = (gates + XCDS - 1) / XCDS * XCDS;
-  if (M <= 128) {
+  // Measured (us; 64 x 32 blocks, 128 x 128 tiles, 256 x 256 tiles):
+  //   D 2048, 32 heads: 64 rows (192 blocks) 9.1 / 13.5, 128 rows (384) 15.8 / 13.7;
+  //   D 768, 12 heads: 128 rows (144 blocks) 5.3 / 7.9, 256 rows (288) 8.7 / 8.1:
+  //   blocks while one round of the compute units has them all;
+  //   D 2048, 32 heads: 1024 rows (96 large tiles) 23.3 / 33.3, 1536 (144) 34.2 / 33.4,
+  //   2048 (192) 37.3 / 33.6, 4096 (384) 68 / 62; D 768, 12 heads: 4096 rows (144)
+  //   17.8 / 16.4, 7168 (252) 27.2 / 21.5, 16384 (576) 52.6 / 53.0: large tiles from
+  //   144 on.
+  if (tiles(FM, FN) <= CUS) {
     hipLaunchKernelGGL(ttt_input_f8_few_k, dim3(static_cast<uint32_t>(gates + tiles(FM, FN))),
                        dim3(512), 0, stream, a);
-  } else if (tiles(256, 256) >= F8Stream::GRID) {
+  } else if (tiles(F8Stream::BM, F8Stream::BN) >= 144) {
     hipLaunchKernelGGL(ttt_input_f8_k, dim3(static_cast<uint32_t>(padded + F8Stream::GRID)),
                        dim3(F8Stream::NT), 0, stream, a);
   } else {
