@@ -130,19 +130,24 @@ __global__ __launch_bounds__(NT, 2) void ttt_ssm_bwd_walk_k(SsmBackwardArgs a) {
   else walk<NI, N, true>(a, lds, blockIdx.x - forward);
 }
 
-// States in front of the segments, and adjoints behind them.
+// States in front of the segments (the first half of the workgroups), and
+// adjoints behind them.
 __global__ __launch_bounds__(NT) void ttt_ssm_bwd_join_k(SsmBackwardArgs a) {
   const SsmArgs& f = a.f;
   const int per = f.N * P / 4;
-  const uint64_t i = static_cast<uint64_t>(blockIdx.x) * NT + threadIdx.x;
+  const bool adjoint = blockIdx.x >= gridDim.x / 2;
+  const uint32_t block = adjoint ? blockIdx.x - gridDim.x / 2 : blockIdx.x;
+  const uint64_t i = static_cast<uint64_t>(block) * NT + threadIdx.x;
   const size_t unit = i / per, at = (i - unit * per) * 4, size = static_cast<size_t>(f.N) * P;
   const double* fades = f.ws_fade + unit * f.segs;
-  const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-  join_segments(f.ws_state + unit * f.segs * size + at, size, fades, f.segs, f.segs - 1, 1,
-                f.state0 ? *reinterpret_cast<const f32x4*>(f.state0 + unit * size + at) : zero);
-  join_segments(a.ws_adj + (unit * f.segs + f.segs - 1) * size + at, size, fades + f.segs - 1,
-                f.segs, f.segs - 1, -1,
-                a.dstate ? *reinterpret_cast<const f32x4*>(a.dstate + unit * size + at) : zero);
+  const float* first = adjoint ? a.dstate : f.state0;
+  const f32x4 S = first ? *reinterpret_cast<const f32x4*>(first + unit * size + at)
+                        : f32x4{0.f, 0.f, 0.f, 0.f};
+  if (adjoint)
+    join_segments(a.ws_adj + (unit * f.segs + f.segs - 1) * size + at, size, fades + f.segs - 1,
+                  f.segs, f.segs - 1, -1, S);
+  else
+    join_segments(f.ws_state + unit * f.segs * size + at, size, fades, f.segs, f.segs - 1, 1, S);
 }
 
 // ---- the gradients ----------------------------------------------------------
@@ -589,7 +594,8 @@ hipError_t bwd_launch(const SsmBackwardArgs& a, hipStream_t stream) {
   hipLaunchKernelGGL((ttt_ssm_bwd_walk_k<NI, N>), dim3(units * (2 * f.segs - 1)), dim3(NT), 0,
                      stream, a);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  hipLaunchKernelGGL(ttt_ssm_bwd_join_k, dim3(units * (N * P / 4 / NT)), dim3(NT), 0, stream, a);
+  hipLaunchKernelGGL(ttt_ssm_bwd_join_k, dim3(2 * units * (N * P / 4 / NT)), dim3(NT), 0, stream,
+                     a);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   hipLaunchKernelGGL((ttt_ssm_bwd_k<NI, N>), dim3(units * f.segs), dim3(GT), 0, stream, a);
   if ((e = hipGetLastError()) != hipSuccess) return e;
