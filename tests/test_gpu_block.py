@@ -163,3 +163,62 @@ def test_a_stream_of_its_own_and_a_stream_argument():
         assert torch.equal(u, v)
     for u, v in zip(g2, g):
         assert (u is None and v is None) or torch.equal(u, v)
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 values in one tensor: the last unit (row) is what it is alone."""
+    H, T = 9, 1 << 22
+    x = torch.empty(1, H, T, 64, dtype=torch.bfloat16, device="cuda")
+    x.normal_()
+    w, bias = rnd(H, 4, 64, scale=0.5), rnd(H, 64)
+    y, tail = fw.ttt_conv_forward(x, w, bias, return_state=True)
+    y1, tail1 = fw.ttt_conv_forward(x[:, -1:].contiguous(), w[-1:], bias[-1:], return_state=True)
+    assert torch.equal(y[:, -1:], y1) and torch.equal(tail[:, -1:], tail1)
+    dx, dw, db, _ = fw.ttt_conv_backward(x, w, bias, y)
+    dx1, dw1, db1, _ = fw.ttt_conv_backward(x[:, -1:].contiguous(), w[-1:], bias[-1:], y1)
+    assert torch.equal(dx[:, -1:], dx1) and torch.equal(dw[-1:], dw1) and torch.equal(db[-1:], db1)
+    del dx, dx1, y1
+    rows = x.view(-1, 8192)
+    weight = torch.ones(8192, device="cuda")
+    n, r = fw.ttt_rms_norm_forward(rows, weight, y.view(-1, 8192))
+    n1, r1 = fw.ttt_rms_norm_forward(rows[-3000:].contiguous(), weight,
+                                     y.view(-1, 8192)[-3000:].contiguous())
+    assert torch.equal(n[-3000:], n1) and torch.equal(r[-3000:], r1)
+    del n, r, y
+    # the scan: the last unit from a state in its middle is the whole scan's end
+    dt = torch.full((1, H, T), 0.05, device="cuda")
+    a = -torch.ones(H, device="cuda")
+    b = torch.empty(1, H, T, 32, dtype=torch.bfloat16, device="cuda")
+    b.normal_(std=0.3)
+    y, S = fw.ttt_ssm_forward(x, dt, a, b, b)
+    part = [t[:, -1:, -576:].contiguous() for t in (x, dt, b)]
+    want = block.ssm(*d64(part[0], part[1], a[-1:], part[2], part[2], None, None))
+    # what came before the last 576 tokens has faded to e^-29, and to e^-14 300 tokens from the end
+    held("state", S[:, -1:], want["state"], want["state_mag"] + 1.0, 2.0 ** -15)
+    held("y", y[:, -1:, -300:], want["y"][:, :, -300:], want["y_mag"][:, :, -300:] + 1.0,
+         2.0 ** -14)
+    dy = torch.flip(y, [2])
+    del y
+    got = fw.ttt_ssm_backward(x, dt, a, b, b, dy)
+    g = block.ssm_backward(*d64(part[0], part[1], a[-1:], part[2], part[2],
+                                dy[:, -1:, -576:].contiguous(), None, None, None))
+    for name, t in zip(("dx", "ddt"), got):
+        held(name, t[:, -1:, -300:], g[name][:, :, -300:], g[name + "_mag"][:, :, -300:] + 1.0,
+             2.0 ** -14)
+
+
+def test_projection_offsets_past_32_bits():
+    """More than 2^31 values of x and of each of q, k, v (T itself is at most 2^22)."""
+    T, D, H = (1 << 21) + 300, 512, 9
+    x = torch.empty(2, T, D, dtype=torch.float8_e4m3fn, device="cuda")
+    x.view(torch.uint8).random_(0, 0x78)      # every positive finite value but the top binade's
+    xs = torch.full((2, T), 2.0 ** -10, device="cuda")
+    w = rnd(3 * H * 64 + H, D, seed=60).to(torch.float8_e4m3fn)
+    ws = torch.full((3 * H * 64 + H,), 2.0 ** -5, device="cuda")
+    be = rnd(H, seed=61, scale=0.1)
+    got = fw.ttt_input_projection_f8(x, xs, w, ws, be, heads=H, eta_base=1 / 64)
+    want = block.input_f8(*d64(x[1:, -300:], xs[1:, -300:], w, ws, be), H, 1 / 64)
+    for name, t in zip("qkv", got):
+        held(name, t[1:, :, -300:], want[name], want[name + "_mag"], 2.0 ** -15)
+    gate = want["gate_mag"] * (D / 32 + 40) * 2.0 ** -24
+    held("eta", got[3][1:, :, -300:], want["eta"], want["eta"] * (gate + 2.0 ** -20), 1.0)
