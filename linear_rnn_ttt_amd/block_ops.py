@@ -152,7 +152,7 @@ def ttt_rms_norm_forward_f8(x: torch.Tensor, weight: torch.Tensor,
     float8_e4m3fn, scale [...] fp32, r); y8 * scale stands for the norm's
     output.  The x and x_scale of ttt_input_projection_f8."""
     io, rows, width, res_out = _norm_args(x, weight, residual, res_out)
-    y = _given("y", y, x.shape, F8, x.device)
+    y = torch.empty_like(x, dtype=F8) if y is None else _check("y", y, F8, x.shape, x.device)
     scale = _given("scale", scale, x.shape[:-1], torch.float32, x.device)
     _call("ttt_rms_norm_forward_f8", x.device, rows, width, io, float(eps), _ptr(x),
           _ptr(residual), _ptr(weight), _ptr(y), _ptr(scale), _ptr(res_out))
@@ -201,7 +201,8 @@ def ttt_input_projection_f8(x: torch.Tensor, x_scale: torch.Tensor, w_in: torch.
     them; a weight's scale is its row's largest magnitude / 448).  Returns
     (q, k, v, eta): q, k, v [B,H,T,d] bf16, eta [B,H,T] fp32.  out: an
     optional tuple of four tensors to write instead."""
-    _dev_tensor("x", x, F8)
+    if not (isinstance(x, torch.Tensor) and x.dtype is F8 and x.is_cuda and x.is_contiguous()):
+        _dev_tensor("x", x, F8)
     if x.dim() != 3:
         raise ValueError("x must be [B, T, D]")
     B, T, D = x.shape
@@ -212,10 +213,14 @@ def ttt_input_projection_f8(x: torch.Tensor, x_scale: torch.Tensor, w_in: torch.
     _check("w_scale", w_scale, torch.float32, (n,), dev)
     _check("b_eta", b_eta, torch.float32, (H,), dev)
     if out is None:
-        out = (None,) * 4
-    q, k, v = (_given(name, t, (B, H, T, d), torch.bfloat16, dev)
-               for name, t in zip(("q", "k", "v"), out[:3]))
-    eta = _given("eta", out[3], (B, H, T), torch.float32, dev)
+        q = torch.empty((B, H, T, d), dtype=torch.bfloat16, device=dev)
+        k, v = torch.empty_like(q), torch.empty_like(q)
+        eta = torch.empty((B, H, T), dtype=torch.float32, device=dev)
+    else:
+        q, k, v, eta = out
+        for name, t in (("q", q), ("k", k), ("v", v)):
+            _check(name, t, torch.bfloat16, (B, H, T, d), dev)
+        _check("eta", eta, torch.float32, (B, H, T), dev)
     p = _lib.TTTParams(B, H, T, d, 16, _lib.TTT_BF16, 0, 0.0, 0)
     _call("ttt_input_projection_f8", dev, ctypes.byref(p), D, _ptr(x), _ptr(x_scale), _ptr(w_in),
           _ptr(w_scale), _ptr(b_eta), float(eta_base), _ptr(q), _ptr(k), _ptr(v), _ptr(eta))
@@ -231,7 +236,9 @@ def _conv_args(x, w, bias, dims):
     B, H, d = x.shape[0], x.shape[1], x.shape[-1]
     T = x.shape[2] if dims == 4 else 1
     dev = x.device
-    _dev_tensor("w", w, torch.float32, device=dev)
+    if not (isinstance(w, torch.Tensor) and w.dtype is torch.float32 and w.device == dev
+            and w.is_contiguous()):
+        _dev_tensor("w", w, torch.float32, device=dev)
     if w.dim() != 3 or w.shape[0] != H or w.shape[2] != d:
         raise ValueError("w must have shape (%d, taps, %d) (got %s)" % (H, d, tuple(w.shape)))
     _optional("bias", bias, torch.float32, (H, d), dev)
@@ -312,7 +319,9 @@ def _ssm_args(x, dt, a, b, c, d_skip, dims):
     dev = x.device
     _check("dt", dt, torch.float32, (B, H) + tuple(t), dev)
     _check("a", a, torch.float32, (H,), dev)
-    _dev_tensor("b", b, x.dtype, device=dev)
+    if not (isinstance(b, torch.Tensor) and b.dtype is x.dtype and b.device == dev
+            and b.is_contiguous()):
+        _dev_tensor("b", b, x.dtype, device=dev)
     if b.dim() != dims or b.shape[0] != B or b.shape[2:-1] != t:
         raise ValueError("b must be [B, groups, T, N] beside x (got %s)" % (tuple(b.shape),))
     _check("c", c, x.dtype, b.shape, dev)

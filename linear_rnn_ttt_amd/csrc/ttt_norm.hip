@@ -10,9 +10,14 @@
 // where each workgroup sums dw over its rows in registers and leaves one
 // partial row; a second launch adds the partial rows in order.
 //
-// Bound by HBM.  A row is spread over one wave (up to 2048 values, 8 per lane
-// and step; no barrier) or, for wider rows and for launches of too few rows to
-// fill the chip with single waves, over the 256 threads of a workgroup.
+// Bound by HBM: forward with residual, bf16, 32768 rows of 2048: 99 us, 5.4 TB/s
+// (a copy on this card reaches 5.4); backward, 16384 rows of 768: 20.7 us with
+// its second launch, 4.9 TB/s.  All of a row's loads go out before the first of
+// them is waited for: reading, widening and adding step by step took 26.7 us
+// for that backward, 530 instead of 432 us for a forward of 16384 rows of 16384.
+// Loading the next row as well, ahead of the sums, gained nothing (21.4 us): there are
+// enough waves.  Backward workgroups: 512, each with a row of partial sums;
+// 256 take 23.2 us, 1024 22.4.
 #include "ttt_block.hpp"
 #include "ttt_block_io.hpp"
 
@@ -29,9 +34,24 @@ template <int LANES>
 struct RowSum {
   __device__ static float sum(float x, float*) { return wave_sum(x); }
   __device__ static float max(float x, float*) { return wave_max(x); }
+  __device__ static void sum2(float* x, float* y, float*, float*) {
+    *x = wave_sum(*x);
+    *y = wave_sum(*y);
+  }
 };
 template <>
 struct RowSum<NT> {
+  __device__ static void sum2(float* x, float* y, float* lds, float* lds2) {
+    *x = wave_sum(*x);
+    *y = wave_sum(*y);
+    if ((threadIdx.x & 63) == 0) {
+      lds[threadIdx.x >> 6] = *x;
+      lds2[threadIdx.x >> 6] = *y;
+    }
+    lds_barrier();
+    *x = (lds[0] + lds[1]) + (lds[2] + lds[3]);
+    *y = (lds2[0] + lds2[1]) + (lds2[2] + lds2[3]);
+  }
   // every thread gets the four waves' total; `lds` has 4 floats, and a second
   // call has to bring another 4
   __device__ static float sum(float x, float* lds) {
@@ -66,15 +86,24 @@ __global__ __launch_bounds__(NT) void ttt_norm_k(NormArgs a) {
   for (int64_t row = static_cast<int64_t>(blockIdx.x) * ROWS + threadIdx.x / LANES; row < a.rows;
        row += step, turn ^= 1) {
     const size_t at = static_cast<size_t>(row) * W;
+    Raw8<BF16> rx[V], rq[RES ? V : 1];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int f = 8 * (lane + LANES * j);
+      if (f < W) {
+        rx[j] = load8_raw<BF16>(a.x, at + f);
+        if constexpr (RES) rq[j] = load8_raw<BF16>(a.residual, at + f);
+      }
+    }
     F8 r[V];
     float ss = 0.f;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int f = 8 * (lane + LANES * j);
       if (f < W) {
-        r[j] = load8<BF16>(a.x, at + f);
+        r[j] = widen8(rx[j]);
         if constexpr (RES) {
-          const F8 q = load8<BF16>(a.residual, at + f);
+          const F8 q = widen8(rq[j]);
 #pragma unroll
           for (int i = 0; i < 8; ++i) r[j].v[i] += q.v[i];
         }
@@ -149,23 +178,30 @@ __global__ __launch_bounds__(NT) void ttt_norm_bwd_k(NormBackwardArgs a) {
   for (int64_t row = static_cast<int64_t>(blockIdx.x) * ROWS + slot; row < a.rows;
        row += step, turn ^= 1) {
     const size_t at = static_cast<size_t>(row) * W;
-    F8 r[V], g[V];
+    Raw8<BF16> rr[V], rg[V], ro[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int f = 8 * (lane + LANES * j);
+      if (f < W) {
+        rr[j] = load8_raw<BF16>(a.r, at + f);
+        rg[j] = load8_raw<BF16>(a.dy, at + f);
+        ro[j] = a.dr ? load8_raw<BF16>(a.dr, at + f) : zero8_raw<BF16>();
+      }
+    }
     float ss = 0.f, su = 0.f;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int f = 8 * (lane + LANES * j);
       if (f < W) {
-        r[j] = load8<BF16>(a.r, at + f);
-        g[j] = load8<BF16>(a.dy, at + f);
+        const F8 r = widen8(rr[j]), g = widen8(rg[j]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          ss += r[j].v[i] * r[j].v[i];
-          su += g[j].v[i] * w[j].v[i] * r[j].v[i];
+          ss += r.v[i] * r.v[i];
+          su += g.v[i] * w[j].v[i] * r.v[i];
         }
       }
     }
-    ss = RowSum<LANES>::sum(ss, red[turn][0]);
-    su = RowSum<LANES>::sum(su, red[turn][1]);
+    RowSum<LANES>::sum2(&ss, &su, red[turn][0], red[turn][1]);
     const float rstd = 1.0f / sqrtf(ss / static_cast<float>(W) + a.eps);
     // xh mean(u xh) rstd = r (rstd^3 sum(u r) / W)
     const float back = rstd * rstd * rstd * (su / static_cast<float>(W));
@@ -173,17 +209,12 @@ __global__ __launch_bounds__(NT) void ttt_norm_bwd_k(NormBackwardArgs a) {
     for (int j = 0; j < V; ++j) {
       const int f = 8 * (lane + LANES * j);
       if (f < W) {
-        F8 o;
-        if (a.dr) {
-          o = load8<BF16>(a.dr, at + f);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) o.v[i] = 0.f;
-        }
+        const F8 r = widen8(rr[j]), g = widen8(rg[j]);
+        F8 o = widen8(ro[j]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          o.v[i] += rstd * g[j].v[i] * w[j].v[i] - r[j].v[i] * back;
-          dw[j].v[i] += g[j].v[i] * (r[j].v[i] * rstd);
+          o.v[i] += rstd * g.v[i] * w[j].v[i] - r.v[i] * back;
+          dw[j].v[i] += g.v[i] * (r.v[i] * rstd);
         }
         store8<BF16>(a.dx, at + f, o);
       }
@@ -217,9 +248,16 @@ __global__ __launch_bounds__(NT) void ttt_norm_bwd_sum_k(NormBackwardArgs a) {
   column_sums(a.partial, a.width, a.groups, [&](size_t f, float s) { a.dweight[f] = s; });
 }
 
-// Widths by the number of 8-value steps that their row takes.
+// A row is one wave's (no barrier) or, where that leaves each lane with too many
+// loads, a workgroup's; V steps of 8 values for each lane.  Measured, bf16, us,
+// a wave / a workgroup a row:
+//   forward     512 rows: width 512 2.1 / 2.2, 768 2.5 / 2.3, 1024 2.6 / 2.4, 2048 3.7 / 2.9
+//             2048 rows:        512 2.7 / 2.9, 768 3.3 / 3.3, 1024 3.7 / 3.6, 2048 6.4 / 6.0
+//             8192 rows:        512 6.0 / 6.1, 768 8.3 / 9.2, 1024 11.1 / 11.5, 2048 20.7 / 20.4
+//   backward    512 rows:       512 4.6 / 6.9, 1024 5.7 / 7.5, 2048 7.6 / 8.0
+//            32768 rows:        512 26.9 / 86, 1024 48.7 / 98, 2048 116 / 155
 constexpr int64_t kMaxGrid = 2048;      // 8 workgroups per compute unit, then rows in turn
-constexpr int64_t kWaveRows = 2048;     // fewer rows: a workgroup each
+constexpr int64_t kWaveRows = 2048;     // forward, widths of 520 to 1024: fewer take workgroups
 
 template <bool BF16, int LANES, int V>
 hipError_t norm_launch(const NormArgs& a, hipStream_t stream) {
@@ -238,11 +276,8 @@ hipError_t norm_launch(const NormArgs& a, hipStream_t stream) {
 template <bool BF16>
 hipError_t norm_pick(const NormArgs& a, hipStream_t stream) {
   const int w = a.width;
-  if (w <= 2048 && a.rows >= kWaveRows) {
-    if (w <= 512) return norm_launch<BF16, 64, 1>(a, stream);
-    if (w <= 1024) return norm_launch<BF16, 64, 2>(a, stream);
-    return norm_launch<BF16, 64, 4>(a, stream);
-  }
+  if (w <= 512) return norm_launch<BF16, 64, 1>(a, stream);
+  if (w <= 1024 && a.rows >= kWaveRows) return norm_launch<BF16, 64, 2>(a, stream);
   if (w <= 2048) return norm_launch<BF16, NT, 1>(a, stream);
   if (w <= 4096) return norm_launch<BF16, NT, 2>(a, stream);
   if (w <= 8192) return norm_launch<BF16, NT, 4>(a, stream);
@@ -263,7 +298,7 @@ hipError_t norm_bwd_pick(const NormBackwardArgs& a, hipStream_t stream) {
   const int w = a.width;
   if (w <= 512) return norm_bwd_launch<BF16, 64, 1>(a, stream);
   if (w <= 1024) return norm_bwd_launch<BF16, 64, 2>(a, stream);
-  if (w <= 2048) return norm_bwd_launch<BF16, NT, 1>(a, stream);
+  if (w <= 2048) return norm_bwd_launch<BF16, 64, 4>(a, stream);
   if (w <= 4096) return norm_bwd_launch<BF16, NT, 2>(a, stream);
   if (w <= 8192) return norm_bwd_launch<BF16, NT, 4>(a, stream);
   return norm_bwd_launch<BF16, NT, 8>(a, stream);
