@@ -49,7 +49,7 @@ template <int NI, int N>
 __global__ __launch_bounds__(NT, 2) void ttt_ssm_states_k(SsmArgs a) {
   constexpr int L = kSsmTile<NI>;
   __shared__ alignas(16) StatesLds<NI, N> lds;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, c = lane & 15;
+  const int tid = threadIdx.x, lane = tid & 63, wave = wave_of(tid), g = lane >> 4, c = lane & 15;
   const Place at(a, blockIdx.x, a.segs - 1);   // nothing follows the last segment
   const int seg = at.seg, h = at.h;
   const size_t unit = at.unit, shared = at.shared;
@@ -127,9 +127,9 @@ struct ScanLds {
 template <int NI, int N>
 __global__ __launch_bounds__(NT, 2) void ttt_ssm_scan_k(SsmArgs a) {
   using Lds = ScanLds<NI, N>;
-  constexpr int L = Lds::L, TB = Lds::TB, NM = Lds::NM;
+  constexpr int L = Lds::L, TB = Lds::TB, NM = Lds::NM, BELOW = TB * (TB - 1) / 2;
   __shared__ alignas(16) Lds lds;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, c = lane & 15;
+  const int tid = threadIdx.x, lane = tid & 63, wave = wave_of(tid), g = lane >> 4, c = lane & 15;
   const Place at(a, blockIdx.x, a.segs);
   const int seg = at.seg, h = at.h;
   const size_t unit = at.unit, shared = at.shared;
@@ -175,19 +175,26 @@ __global__ __launch_bounds__(NT, 2) void ttt_ssm_scan_k(SsmArgs a) {
     step = steps_of(tile + 2);
 
     // M^T block by block: (b_s . c_t), decayed and masked
-    for (int i = wave; i < Lds::BLOCKS; i += 4) {
-      int tb, sb;
-      block_of(i, &tb, &sb);
+    auto make = [&](int tb, int sb) {
       f32x4 m = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int k = 0; k < N / 32; ++k)
         m = mfma_parts(lds.b.rows8(16 * sb, 32 * k, g, c), lds.c.rows8(16 * tb, 32 * k, g, c), m);
-      m *= tk.fades(tb, 16 * tb + c, 16 * sb + 4 * g) * tk.steps(16 * sb + 4 * g);
-      if (tb == sb) {   // d x_t, as a product too
+      return m * (tk.fades(tb, sb, 16 * tb + c, 16 * sb + 4 * g) * tk.steps(16 * sb + 4 * g));
+    };
+    if (TB == 4 || wave < TB) {
+      f32x4 m = make(wave, wave);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) m[r] += 4 * g + r == c ? skip : 0.f;
+      for (int r = 0; r < 4; ++r) m[r] += 4 * g + r == c ? skip : 0.f;   // d x_t, as a product too
+      lds.m.put(wave * (wave + 3) / 2, lane, m);
+    }
+    if (wave < 3) {   // wave 3 makes decays instead
+      for (int o = (wave + 1) % 3; o < BELOW; o += 3) {
+        int tb, sb;
+        block_of(o, &tb, &sb);
+        ++tb;
+        lds.m.put(tb * (tb + 1) / 2 + sb, lane, make(tb, sb));
       }
-      lds.m.put(i, lane, m);
     }
 
     // Y^T of the wave's features: from the state in front of the tile

@@ -395,7 +395,7 @@ __global__ __launch_bounds__(GT, NI == 1 && N <= 64 ? 4 : 2) void ttt_ssm_bwd_k(
         xt = mfma_parts(lds.x.rows8(16 * sb, 32 * k, g, c), lds.dy.rows8(16 * tb, 32 * k, g, c),
                         xt);
       const int t = 16 * tb + c, s0 = 16 * sb + 4 * g;
-      const f32x4 fade = tk.fades(tb, t, s0), dt = tk.steps(s0);
+      const f32x4 fade = tk.fades(tb, sb, t, s0), dt = tk.steps(s0);
       const f32x4 z = gt * xt * fade;
       f32x4 w1 = gt * (fade * dt), w2 = xt * (fade * dt);
       float row = 0.f;

@@ -149,10 +149,13 @@ struct Plane {
 };
 
 // A range of memory for buffer loads and stores: reads past `bytes` give zero,
-// stores past it do nothing, so a tile's missing rows need no branches.
+// stores past it do nothing, so a tile's missing rows need no branches.  `bytes`
+// is the same in every lane; made a scalar here, as a clamp (a vector instruction)
+// would put it, and with it the descriptor, in vector registers and a loop
+// around every access.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(const void* p, int bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), static_cast<short>(0), bytes,
-                                           0x00020000);
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), static_cast<short>(0),
+                                           __builtin_amdgcn_readfirstlane(bytes), 0x00020000);
 }
 
 // A tile's rows on their way from memory: 16 bytes per vector, rows from
@@ -288,9 +291,9 @@ struct alignas(16) Tokens {
     return all;
   }
   // exp of the decay exponents summed over tokens s+1 .. t for s = s0 .. s0 + 3
-  // and one t of block tb; 0 where s > t
-  __device__ __forceinline__ f32x4 fades(int tb, int t, int s0) const {
-    if (s0 < 16 * tb) return *reinterpret_cast<const f32x4*>(&col[tb - 1][s0]) * row[t];
+  // of block sb and one t of block tb; 0 where s > t
+  __device__ __forceinline__ f32x4 fades(int tb, int sb, int t, int s0) const {
+    if (sb < tb) return *reinterpret_cast<const f32x4*>(&col[tb - 1][s0]) * row[t];
     const f32x4 h = *reinterpret_cast<const f32x4*>(&hi[s0]);
     const f32x4 l = *reinterpret_cast<const f32x4*>(&lo[s0]);
     f32x4 w;
@@ -339,6 +342,10 @@ template <int NI>
 __device__ __forceinline__ const char* row_ptr(const void* p, size_t row, int width) {
   return static_cast<const char*>(p) + row * width * (NI == 1 ? 2 : 4);
 }
+
+// The wave's number as a scalar, so that what depends on it alone is worked out
+// once per wave and branches on it are branches.
+__device__ __forceinline__ int wave_of(int tid) { return __builtin_amdgcn_readfirstlane(tid >> 6); }
 
 // A lane index that the compiler takes for a new value: LDS addresses made from
 // it are made where they are used and not kept in registers around the loop.
