@@ -37,6 +37,14 @@ constexpr int NT = SSM_NT, P = SSM_P;
 
 // ---- what each segment adds to a state of zero ------------------------------
 
+// A segment's state in the workspace, in the order of the registers that hold
+// it: vector 64 i is rows 16 i + 4 g .. 4 g + 3 of the lane's feature.
+__device__ __forceinline__ f32x4* seg_state(const SsmArgs& a, size_t unit, int seg, int wave,
+                                            int lane, int N) {
+  return reinterpret_cast<f32x4*>(a.ws_state + (unit * a.segs + seg) * (N * P)) +
+         wave * (N / 16) * 64 + lane;
+}
+
 template <int NI, int N>
 struct StatesLds {
   static constexpr int L = kSsmTile<NI>;
@@ -93,21 +101,30 @@ __global__ __launch_bounds__(NT, 2) void ttt_ssm_states_k(SsmArgs a) {
     work(tile, next);
     if (tile + 1 < end) work(tile + 1, after);
   }
-  float* out = a.ws_state + (unit * a.segs + seg) * (N * P);
+  f32x4* out = seg_state(a, unit, seg, wave, lane, N);
 #pragma unroll
-  for (int i = 0; i < N / 16; ++i)
-#pragma unroll
-    for (int r = 0; r < 4; ++r) out[(16 * i + 4 * g + r) * P + 16 * wave + c] = S[i][r];
+  for (int i = 0; i < N / 16; ++i) out[64 * i] = S[i];
   if (tid == 0) a.ws_fade[unit * a.segs + seg] = total;
 }
 
-// ws_state[seg]: from what the segment adds to the state in front of it.
+// ws_state[seg]: from what the segment adds to the state in front of it.  For
+// up to kScanJoins segments the scan does this itself, each workgroup for its own
+// start, in place of this launch: 121.0 -> 116.1 us for the whole call at B4 H32
+// T4096 N128 (4 segments); at B4 H32 T8192 N64 (8 segments) it would cost, 179.9 -> 185.8.
+constexpr int kScanJoins = 4;
 __global__ __launch_bounds__(NT) void ttt_ssm_join_k(SsmArgs a) {
   const int per = a.N * P / 4;   // 16-byte vectors of a state: a multiple of NT
   const uint64_t i = static_cast<uint64_t>(blockIdx.x) * NT + threadIdx.x;
   const size_t unit = i / per, at = (i - unit * per) * 4, size = static_cast<size_t>(a.N) * P;
   f32x4 S = {0.f, 0.f, 0.f, 0.f};
-  if (a.state0) S = *reinterpret_cast<const f32x4*>(a.state0 + unit * size + at);
+  if (a.state0) {   // at as in seg_state
+    const int lane = at / 4 & 63, block = at / 256, wave = block / (a.N / 16);
+    const float* from = a.state0 + unit * size +
+                        (16 * (block - wave * (a.N / 16)) + 4 * (lane >> 4)) * P + 16 * wave +
+                        (lane & 15);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) S[r] = from[r * P];
+  }
   join_segments(a.ws_state + unit * a.segs * size + at, size, a.ws_fade + unit * a.segs, a.segs,
                 a.segs - 1, 1, S);
 }
@@ -137,13 +154,36 @@ __global__ __launch_bounds__(NT, 2) void ttt_ssm_scan_k(SsmArgs a) {
   const int first = seg * a.seg_tiles, end = min(first + a.seg_tiles, tiles);
   const float ah = a.a[h], skip = a.d_skip ? a.d_skip[h] : 0.f;
   f32x4 S[N / 16];
-  const float* from = a.segs > 1 ? a.ws_state + (unit * a.segs + seg) * (N * P)
-                                 : a.state0 ? a.state0 + unit * (N * P) : nullptr;
+  if (a.segs > kScanJoins) {
+    const f32x4* from = seg_state(a, unit, seg, wave, lane, N);
 #pragma unroll
-  for (int i = 0; i < N / 16; ++i)
+    for (int i = 0; i < N / 16; ++i) S[i] = from[64 * i];
+  } else {
+    const float* from = a.state0 ? a.state0 + unit * (N * P) : nullptr;
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
-      S[i][r] = from ? from[(16 * i + 4 * g + r) * P + 16 * wave + c] : 0.f;
+    for (int i = 0; i < N / 16; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        S[i][r] = from ? from[(16 * i + 4 * g + r) * P + 16 * wave + c] : 0.f;
+    constexpr int AT_ONCE = 256 / N;   // segments whose loads are issued together
+    for (int s0 = 0; s0 < seg; s0 += AT_ONCE) {
+      f32x4 added[AT_ONCE][N / 16];
+#pragma unroll
+      for (int k = 0; k < AT_ONCE; ++k)
+        if (s0 + k < seg) {
+          const f32x4* p = seg_state(a, unit, s0 + k, wave, lane, N);
+#pragma unroll
+          for (int i = 0; i < N / 16; ++i) added[k][i] = p[64 * i];
+        }
+#pragma unroll
+      for (int k = 0; k < AT_ONCE; ++k)
+        if (s0 + k < seg) {
+          const float fade = exp2_raw(static_cast<float>(a.ws_fade[unit * a.segs + s0 + k]));
+#pragma unroll
+          for (int i = 0; i < N / 16; ++i) S[i] = S[i] * fade + added[k][i];
+        }
+    }
+  }
   struct Tile {
     Fetch<NI, L, P, NT> x;
     Fetch<NI, L, N, NT> b, c;
@@ -304,8 +344,10 @@ hipError_t scan_launch(const SsmArgs& a, hipStream_t stream) {
     hipLaunchKernelGGL((ttt_ssm_states_k<NI, N>), dim3(units * (a.segs - 1)), dim3(NT), 0, stream,
                        a);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    hipLaunchKernelGGL(ttt_ssm_join_k, dim3(units * (N * P / 4 / NT)), dim3(NT), 0, stream, a);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
+    if (a.segs > kScanJoins) {
+      hipLaunchKernelGGL(ttt_ssm_join_k, dim3(units * (N * P / 4 / NT)), dim3(NT), 0, stream, a);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
   }
   hipLaunchKernelGGL((ttt_ssm_scan_k<NI, N>), dim3(units * a.segs), dim3(NT), 0, stream,
                      a);
