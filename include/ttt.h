@@ -588,8 +588,9 @@ ttt_status ttt_conv_decode_step(const ttt_params* p, int32_t taps, uint32_t flag
 uint64_t ttt_conv_backward_workspace_bytes(const ttt_params* p, int32_t taps);
 
 /*
- * Gradients of sum(dy * y) [+ sum(dstate * state_out)]; B*H times the chunks of
- * 256 tokens at most 2^22 (else TTT_ERR_SHAPE):
+ * Gradients of sum(dy * y) [+ sum(dstate * state_out)]; B*H times the chunks
+ * at most 2^22 (else TTT_ERR_SHAPE), a chunk being 16 floor(1024 / d) tokens, at
+ * least 64 (256 for d = 64):
  *   dy      [B,H,T,d] io_dtype.         dstate [B,H,K-1,d] io_dtype or NULL.
  *   dx      [B,H,T,d] io_dtype.         dw [H,K,d], dbias [H,d] fp32 (summed
  *           over the batch; dbias also where bias is NULL).

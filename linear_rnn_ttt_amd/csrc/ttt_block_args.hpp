@@ -57,7 +57,12 @@ struct ConvArgs {
   int32_t B, H, T, d, taps, silu;
 };
 
-constexpr int32_t kConvChunk = 256;   // tokens of one partial filter gradient
+// Tokens of one partial filter gradient, a workgroup's: 16 for each of the rows
+// of d / 4 threads that 256 threads make, at least 64.
+inline int32_t conv_chunk(int32_t d) {
+  const int32_t tokens = 256 / (d / 4) * 16;
+  return tokens < 64 ? 64 : tokens;
+}
 
 struct ConvBackwardArgs {
   const void* x;
@@ -71,7 +76,7 @@ struct ConvBackwardArgs {
   float* dbias;           // [H,d]
   void* dstate0;          // [B,H,K-1,d] io or nullptr
   float* partial;         // [B][chunks][H][K+1][d]
-  int32_t B, H, T, d, taps, silu, chunks;
+  int32_t B, H, T, d, taps, silu, chunk, chunks;
 };
 
 struct SsmArgs {

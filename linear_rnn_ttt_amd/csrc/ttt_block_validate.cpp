@@ -99,7 +99,8 @@ ttt_status check_conv(const ttt_params* p, int32_t taps, uint32_t flags, uint64_
 }
 
 int32_t conv_chunks(const ttt_params* p) {
-  return (p->T + tttk::kConvChunk - 1) / tttk::kConvChunk;
+  const int32_t chunk = tttk::conv_chunk(p->d);
+  return (p->T + chunk - 1) / chunk;
 }
 
 // ---- scan ----
@@ -387,7 +388,7 @@ ttt_status conv_backward(const ttt_params* p, int32_t taps, uint32_t flags, cons
     return TTT_ERR_ALIAS;
   *a = tttk::ConvBackwardArgs{x, w, bias, state0, dy, dstate, dx, dw, dbias, dstate0,
                               static_cast<float*>(workspace), p->B, p->H, p->T, p->d, taps,
-                              (flags & TTT_CONV_SILU) ? 1 : 0, conv_chunks(p)};
+                              (flags & TTT_CONV_SILU) ? 1 : 0, tttk::conv_chunk(p->d), conv_chunks(p)};
   return TTT_OK;
 }
 

@@ -11,7 +11,8 @@
 // features (16 bytes) over a strip of tokens and keeps the window of K inputs
 // in registers, so x comes from HBM once; the K - 1 inputs in front of a strip
 // are the neighbouring strip's lines, in cache.  The loads of a strip are
-// issued together before any of them is used.
+// issued together before any of them is used.  bf16, 4 taps, SiLU, B4 H32 T8192
+// d64: 51 us, 5.3 TB/s (a copy on this card reaches 5.4).
 #include <type_traits>
 
 #include "ttt_block.hpp"
@@ -21,7 +22,7 @@ namespace tttk {
 namespace {
 
 constexpr int NT = 256;
-constexpr int S = 8;              // tokens of a strip (4, 8, 16: forward 55, 54, 59 us, backward 27, 24, 40 us)
+constexpr int S = 8;   // tokens loaded together (4, 8, 16: forward 55, 54, 59 us, backward 27, 24, 40 us)
 constexpr uint32_t MAX_GRID = 1u << 20;
 
 // v_exp_f32 and v_rcp_f32, one unit each: far below what the tests' fp32 bound
@@ -145,14 +146,15 @@ __global__ __launch_bounds__(NT) void ttt_conv_step_k(ConvArgs a) {
     store8<BF16>(a.state_out, (unit * (K - 1) + j) * d + f, widen8(win[j + 1]));
 }
 
-// Backward: a workgroup takes one unit's chunk of tokens.  Threads are
-// (strip of S tokens) x (4 features: with 8 the windows of x, dy and du took
-// over 256 registers and left one wave per SIMD; 38.6 -> 23.6 us at B8 H12
-// T2048); where a chunk's strips do not fit at once they take turns.  The
-// filter gradients are summed over a thread's strips in registers, over the
-// workgroup's strips through LDS and left as one partial [K+1][d] per chunk.
-constexpr int CHUNK = kConvChunk;
-
+// Backward: a workgroup takes one unit's chunk of tokens.  Threads are (run of
+// tokens) x (4 features: with 8 the windows of x, dy and du took over 256
+// registers and left one wave per SIMD, 38.6 us at B8 H12 T2048).  A thread
+// walks its run (16 tokens, more where d / 4 threads hardly fit) keeping the
+// windows, so the K - 1 cotangents behind a run, of which dx needs du again,
+// cost 3 in 19 steps (strips of 8 on their own: 25.1 instead of 23.3 us with
+// the sum's launch).  The filter gradients are summed over a run in registers,
+// over the workgroup's runs through LDS and left as one partial [K+1][d] per
+// chunk.  Bound by the vector unit (u, its sigmoid and slope again), 84 % busy.
 template <bool BF16>
 using Raw4 = std::conditional_t<BF16, u32x2, f32x4>;
 
@@ -201,31 +203,28 @@ __global__ __launch_bounds__(NT) void ttt_conv_bwd_k(ConvBackwardArgs a) {
     for (int j = 0; j < K; ++j)
       w[j] = *reinterpret_cast<const f32x4*>(a.w + (static_cast<size_t>(h) * K + j) * d + f);
     if (a.bias) bias = *reinterpret_cast<const f32x4*>(a.bias + static_cast<size_t>(h) * d + f);
-    for (int strip = row; strip < CHUNK / S; strip += rows) {
-      const int t0 = chunk * CHUNK + strip * S;
-      if (t0 >= T) break;
-      // inputs t0-K+1 .. t0+S+K-2 and cotangents t0 .. t0+S+K-2
-      Raw4<BF16> in[S + 2 * (K - 1)], g[S + K - 1];
-#pragma unroll
-      for (int s = 0; s < S + 2 * (K - 1); ++s) in[s] = input(t0 + s - (K - 1));
-#pragma unroll
-      for (int s = 0; s < S + K - 1; ++s)
-        g[s] = t0 + s < T ? load4_raw<BF16>(a.dy, (unit * T + t0 + s) * d + f) : Raw4<BF16>{};
+    const int share = (a.chunk / S + rows - 1) / rows * S;   // tokens of a thread, one after another
+    const int t0 = chunk * a.chunk + row * share;
+    const int stop = min(min(t0 + share, (chunk + 1) * a.chunk), T);
+    if (t0 < stop) {
+      auto cotangent = [&](int t) {
+        return t < T ? load4_raw<BF16>(a.dy, (unit * T + t) * d + f) : Raw4<BF16>{};
+      };
       f32x4 win[K], dus[K];   // dus[j] = du of token (current - (K-1) + j)
 #pragma unroll
-      for (int j = 0; j < K - 1; ++j) win[j + 1] = to_f32<BF16>(in[j]);
+      for (int j = 0; j < K - 1; ++j) win[j + 1] = to_f32<BF16>(input(t0 + j - (K - 1)));
 #pragma unroll
       for (int j = 0; j < K; ++j) dus[j] = zero;
       const bool first = t0 == 0 && a.dstate0;
-#pragma unroll
-      for (int s = 0; s < S + K - 1; ++s) {
+      // token t, and dx of token t - (K-1), whose du's are then dus[0..K-1]
+      auto step = [&](int t, Raw4<BF16> in, Raw4<BF16> g) {
 #pragma unroll
         for (int j = 0; j < K - 1; ++j) {
           win[j] = win[j + 1];
           dus[j] = dus[j + 1];
         }
-        win[K - 1] = to_f32<BF16>(in[s + K - 1]);
-        f32x4 du = to_f32<BF16>(g[s]);
+        win[K - 1] = to_f32<BF16>(in);
+        f32x4 du = to_f32<BF16>(g);
         if (a.silu) {
           f32x4 u = bias;
 #pragma unroll
@@ -237,24 +236,43 @@ __global__ __launch_bounds__(NT) void ttt_conv_bwd_k(ConvBackwardArgs a) {
           }
         }
         dus[K - 1] = du;
-        if (s < S && t0 + s < T) {
+        if (t < stop) {
           acc[K] += du;
 #pragma unroll
           for (int j = 0; j < K; ++j) acc[j] += du * win[j];
         }
-        // dx of token t0 + s - (K-1): its du's are dus[0..K-1]
-        const int t = t0 + s - (K - 1);
-        if ((s >= K - 1 && t < T) || (first && s < K - 1)) {
+        const int to = t - (K - 1);
+        if ((to >= t0 && to < stop) || (first && to < 0)) {
           f32x4 dx = zero;
 #pragma unroll
           for (int j = 0; j < K; ++j) dx += w[K - 1 - j] * dus[j];
-          if (a.dstate && t >= T - (K - 1))   // also an input of the final state
+          if (a.dstate && to >= T - (K - 1))   // also an input of the final state
             dx += to_f32<BF16>(
-                load4_raw<BF16>(a.dstate, (unit * (K - 1) + (t - (T - (K - 1)))) * d + f));
-          if (t >= 0) store4<BF16>(a.dx, (unit * T + t) * d + f, dx);
-          else store4<BF16>(a.dstate0, (unit * (K - 1) + (t + K - 1)) * d + f, dx);
+                load4_raw<BF16>(a.dstate, (unit * (K - 1) + (to - (T - (K - 1)))) * d + f));
+          if (to >= 0) store4<BF16>(a.dx, (unit * T + to) * d + f, dx);
+          else store4<BF16>(a.dstate0, (unit * (K - 1) + (to + K - 1)) * d + f, dx);
         }
+      };
+      for (int t = t0; t < stop; t += S) {
+        Raw4<BF16> in[S], g[S];
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+          in[s] = input(t + s);
+          g[s] = cotangent(t + s);
+        }
+#pragma unroll
+        for (int s = 0; s < S; ++s) step(t + s, in[s], g[s]);
       }
+      // the cotangents behind that reach back into the share
+      const int last = (stop - t0 + S - 1) / S * S + t0;
+      Raw4<BF16> in[K - 1], g[K - 1];
+#pragma unroll
+      for (int s = 0; s < K - 1; ++s) {
+        in[s] = input(last + s);
+        g[s] = cotangent(last + s);
+      }
+#pragma unroll
+      for (int s = 0; s < K - 1; ++s) step(last + s, in[s], g[s]);
     }
 #pragma unroll
     for (int j = 0; j <= K; ++j)
