@@ -113,7 +113,8 @@ struct Segments {
   int32_t tiles, segs, seg_tiles;
 };
 
-// Time segments of one unit: as many as fill the card once.
+// Time segments of one unit: as many as fill the card once (B4 H32 T8192 N64, four
+// workgroups a compute unit: the scan alone with 4, 6, 8 segments 159, 144, 124 us).
 Segments ssm_segments(const ttt_params* p, uint64_t workgroups) {
   const uint64_t units = static_cast<uint64_t>(p->B) * p->H;
   const int32_t tile = ssm_tile(p);
