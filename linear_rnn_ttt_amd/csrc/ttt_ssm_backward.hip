@@ -388,7 +388,7 @@ __global__ __launch_bounds__(GT, NI == 1 && N <= 64 ? 4 : 2) void ttt_ssm_bwd_k(
 
     // W1 and W2 block by block
     g = anew(g0), c = anew(c0);
-    for (int i = full_wave; i < Lds::BLOCKS; i += GT / 64) {
+    for (int i = full_wave; i < Lds::BLOCKS && full_wave < 6; i += 6) {   // 6, 7: see below
       int tb, sb;
       block_of(i, &tb, &sb);
       f32x4 gt = zero, xt = zero;   // rows s, columns t
@@ -404,19 +404,20 @@ __global__ __launch_bounds__(GT, NI == 1 && N <= 64 ? 4 : 2) void ttt_ssm_bwd_k(
       const f32x4 fade = tk.fades(tb, sb, t, s0), dt = tk.steps(s0);
       const f32x4 z = gt * xt * fade;
       f32x4 w1 = gt * (fade * dt), w2 = xt * (fade * dt);
-      float row = 0.f;
-      f32x4 off;
+      f32x4 off = z;
+      if (tb == sb) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const bool diagonal = tb == sb && 4 * g + r == c;
-        if (diagonal) {
-          lds.zdiag[e][t] = z[r];
-          dd_sum += xt[r];
-          w1[r] += skip;
-        }
-        off[r] = diagonal ? 0.f : z[r];
-        row += off[r] * dt[r];
+        for (int r = 0; r < 4; ++r)
+          if (4 * g + r == c) {
+            lds.zdiag[e][t] = z[r];
+            off[r] = 0.f;
+            dd_sum += xt[r];
+            w1[r] += skip;
+          }
       }
+      float row = 0.f;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) row += off[r] * dt[r];
       const float col = row_sums4(off, c);
       if (c < 4) lds.zcol[e][i][4 * g + c] = col;
       row = group_sum(row);
@@ -439,7 +440,7 @@ __global__ __launch_bounds__(GT, NI == 1 && N <= 64 ? 4 : 2) void ttt_ssm_bwd_k(
         lds.w2.put4(k, t, s0, u32x2{0u, 0u});
       }
     }
-    // by waves with one block: the tile behind is finished, the one before prepared
+    // by waves without blocks: the tile behind is finished, the one before prepared
     if (full_wave == 6) {
       if (tile < end - 1) finish(tile + 1, done_dt, done_fade);
       done_dt = lane < L ? tk.dt[lane] : 0.f;
