@@ -112,11 +112,18 @@ __global__ __launch_bounds__(NT, 2) void ttt_ssm_states_k(SsmArgs a) {
   if (tid == 0) a.ws_fade[unit * a.segs + seg] = total;
 }
 
-// ws_state[seg]: from what the segment adds to the state in front of it.  For
-// up to kScanJoins segments the scan does this itself, each workgroup for its own
-// start, in place of this launch: 121.0 -> 116.1 us for the whole call at B4 H32
-// T4096 N128 (4 segments); at B4 H32 T8192 N64 (8 segments) it would cost, 179.9 -> 185.8.
+// Up to kScanJoins segments the scan's workgroups work their own start out from
+// what the segments add, in place of the join's launch: 121.0 -> 116.1 us for the
+// whole call at B4 H32 T4096 N128 (4 segments); at B4 H32 T8192 N64 (8 segments) it
+// would cost, 179.9 -> 185.8.  Where the final state takes state0's place, though,
+// a segment's workgroup may end before another one has read state0: the join
+// reads it first.
 constexpr int kScanJoins = 4;
+__host__ __device__ inline bool join_launched(const SsmArgs& a) {
+  return a.segs > kScanJoins || (a.segs > 1 && a.state0 && a.state0 == a.state_out);
+}
+
+// ws_state[seg]: from what the segment adds to the state in front of it.
 __global__ __launch_bounds__(NT) void ttt_ssm_join_k(SsmArgs a) {
   const int per = a.N * P / 4;   // 16-byte vectors of a state: a multiple of NT
   const uint64_t i = static_cast<uint64_t>(blockIdx.x) * NT + threadIdx.x;
@@ -159,7 +166,7 @@ __global__ __launch_bounds__(NT, 2) void ttt_ssm_scan_k(SsmArgs a) {
   const int first = seg * a.seg_tiles, end = min(first + a.seg_tiles, tiles);
   const float ah = a.a[h], skip = a.d_skip ? a.d_skip[h] : 0.f;
   f32x4 S[N / 16];
-  if (a.segs > kScanJoins) {
+  if (join_launched(a)) {
     const f32x4* from = seg_state(a, unit, seg, wave, lane, N);
 #pragma unroll
     for (int i = 0; i < N / 16; ++i) S[i] = from[64 * i];
@@ -350,7 +357,7 @@ hipError_t scan_launch(const SsmArgs& a, hipStream_t stream) {
     hipLaunchKernelGGL((ttt_ssm_states_k<NI, N>), dim3(units * (a.segs - 1)), dim3(NT), 0, stream,
                        a);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    if (a.segs > kScanJoins) {
+    if (join_launched(a)) {
       hipLaunchKernelGGL(ttt_ssm_join_k, dim3(units * (N * P / 4 / NT)), dim3(NT), 0, stream, a);
       if ((e = hipGetLastError()) != hipSuccess) return e;
     }

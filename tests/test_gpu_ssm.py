@@ -127,6 +127,19 @@ def test_prompt_cut_in_two_and_in_place_state():
     held("state", S, want["state"], want["state_mag"], STATE)
 
 
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+@pytest.mark.parametrize("T", [90, 250, 700])
+def test_in_place_state_of_any_number_of_segments(T, dtype):
+    """The final state written over state0, which other workgroups of the unit
+    read: bit for bit the state and outputs of a call with two tensors."""
+    x, dt, a, b, c, d, s0 = make(2, 3, 1, T, 64, dtype, seed=17)
+    y, want = ttt_ssm_forward(x, dt, a, b, c, d, state0=s0)
+    for _ in range(4):
+        S = s0.clone()
+        y2, S2 = ttt_ssm_forward(x, dt, a, b, c, d, state0=S, state_out=S)
+        assert S2 is S and torch.equal(S, want) and torch.equal(y2, y)
+
+
 def test_steps_of_zero_leave_the_state():
     """A padded batch: tokens with dt = 0 behind a sequence's end."""
     x, dt, a, b, c, d, s0 = make(2, 3, 1, 140, 64, torch.bfloat16, seed=6)
