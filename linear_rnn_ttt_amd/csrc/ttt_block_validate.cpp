@@ -114,7 +114,12 @@ struct Segments {
 };
 
 // Time segments of one unit: as many as fill the card once (B4 H32 T8192 N64, four
-// workgroups a compute unit: the scan alone with 4, 6, 8 segments 159, 144, 124 us).
+// workgroups a compute unit: the scan alone with 4, 6, 8 segments 159, 144, 124 us),
+// but for few units at most sqrt(40 tiles): the segments are joined one after
+// another, the tiles of a segment worked on one after another, and a tile takes the
+// time of some 40 joins.  N64 bf16, us, with 20 / 40 / 80 / no limit:
+//   forward  B1 H2 T16384 32.2 / 32.8 / 35.3 / 50.5, B1 H1 T131072 73 / 71 / 84 / 159
+//   backward              54.0 / 51.2 / 49.5 / 63.1                127 / 118 / 135 / 142
 Segments ssm_segments(const ttt_params* p, uint64_t workgroups) {
   const uint64_t units = static_cast<uint64_t>(p->B) * p->H;
   const int32_t tile = ssm_tile(p);
@@ -122,6 +127,8 @@ Segments ssm_segments(const ttt_params* p, uint64_t workgroups) {
   s.tiles = (p->T + tile - 1) / tile;
   uint64_t segs = workgroups / units;
   if (segs > static_cast<uint64_t>(s.tiles)) segs = s.tiles;
+  const uint64_t most = static_cast<uint64_t>(std::sqrt(40.0 * s.tiles));
+  if (segs > most) segs = most;
   if (segs < 1) segs = 1;
   s.seg_tiles = static_cast<int32_t>((s.tiles + segs - 1) / segs);
   s.segs = (s.tiles + s.seg_tiles - 1) / s.seg_tiles;

@@ -113,9 +113,9 @@ __global__ __launch_bounds__(NT, 2) void ttt_ssm_states_k(SsmArgs a) {
 }
 
 // Up to kScanJoins segments the scan's workgroups work their own start out from
-// what the segments add, in place of the join's launch: 121.0 -> 116.1 us for the
-// whole call at B4 H32 T4096 N128 (4 segments); at B4 H32 T8192 N64 (8 segments) it
-// would cost, 179.9 -> 185.8.  Where the final state takes state0's place, though,
+// what the segments add, in place of the join's launch: 124.4 -> 120.5 us for the
+// whole call at B4 H32 T4096 N128, 36.9 -> 32.3 at T512 (4 segments); at B4 H32 T8192
+// N64 (8 segments) it would cost, 185.8 -> 193.4.  Where the final state takes state0's place, though,
 // a segment's workgroup may end before another one has read state0: the join
 // reads it first.
 constexpr int kScanJoins = 4;
@@ -125,9 +125,8 @@ __host__ __device__ inline bool join_launched(const SsmArgs& a) {
 
 // ws_state[seg]: from what the segment adds to the state in front of it.
 __global__ __launch_bounds__(NT) void ttt_ssm_join_k(SsmArgs a) {
-  const int per = a.N * P / 4;   // 16-byte vectors of a state: a multiple of NT
-  const uint64_t i = static_cast<uint64_t>(blockIdx.x) * NT + threadIdx.x;
-  const size_t unit = i / per, at = (i - unit * per) * 4, size = static_cast<size_t>(a.N) * P;
+  const JoinPlace place(a.N, blockIdx.x, threadIdx.x);
+  const size_t unit = place.unit, at = place.at, size = static_cast<size_t>(a.N) * P;
   f32x4 S = {0.f, 0.f, 0.f, 0.f};
   if (a.state0) {   // at as in seg_state
     const int lane = at / 4 & 63, block = at / 256, wave = block / (a.N / 16);

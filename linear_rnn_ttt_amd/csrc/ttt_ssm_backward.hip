@@ -140,11 +140,10 @@ __global__ __launch_bounds__(NT, 2) void ttt_ssm_bwd_walk_k(SsmBackwardArgs a) {
 // adjoints behind them.
 __global__ __launch_bounds__(NT) void ttt_ssm_bwd_join_k(SsmBackwardArgs a) {
   const SsmArgs& f = a.f;
-  const int per = f.N * P / 4;
   const bool adjoint = blockIdx.x >= gridDim.x / 2;
   const uint32_t block = adjoint ? blockIdx.x - gridDim.x / 2 : blockIdx.x;
-  const uint64_t i = static_cast<uint64_t>(block) * NT + threadIdx.x;
-  const size_t unit = i / per, at = (i - unit * per) * 4, size = static_cast<size_t>(f.N) * P;
+  const JoinPlace place(f.N, block, threadIdx.x);
+  const size_t unit = place.unit, at = place.at, size = static_cast<size_t>(f.N) * P;
   const double* fades = f.ws_fade + unit * f.segs;
   const float* first = adjoint ? a.dstate : f.state0;
   const f32x4 S = first ? *reinterpret_cast<const f32x4*>(first + unit * size + at)

@@ -394,23 +394,42 @@ __device__ __forceinline__ void add_tile(f32x4 (&S)[COUNT], const Plane<NI, L, N
   }
 }
 
+// Which unit and place in its state (N P / 4 vectors, 256 a workgroup) a thread
+// of a joining workgroup takes.
+struct JoinPlace {
+  size_t unit, at;
+  __device__ __forceinline__ JoinPlace(int N, uint32_t block, int tid) {
+    const uint32_t each = N * SSM_P / 4 / SSM_NT, u = __builtin_amdgcn_readfirstlane(block / each);
+    unit = u;
+    at = 4 * ((block - u * each) * SSM_NT + tid);
+  }
+};
+
 // The states of segments, each slot (`size` floats apart) holding what its
 // segment adds, become the states in front of them, starting from S;
 // `count` segments' additions are used and `slots` slots written.  dir = 1:
 // first segment to last, -1: last to first.  Returns the state behind.  The
-// loads of eight segments are issued together.
+// loads of sixteen segments are issued together; the fades, the same in every
+// lane and written by an earlier launch, go through scalar loads.
 __device__ __forceinline__ f32x4 join_segments(float* p, int64_t size, const double* fades,
                                                int slots, int count, int dir, f32x4 S) {
-  for (int s0 = 0; s0 < slots; s0 += 8) {
-    f32x4 added[8];
+  constexpr int AT_ONCE = 16;
+  typedef __attribute__((address_space(4))) const double* constant;
+  const constant scalar = (constant)fades;
+  for (int s0 = 0; s0 < slots; s0 += AT_ONCE) {
+    f32x4 added[AT_ONCE];
+    float fade[AT_ONCE];
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (s0 + k < count) added[k] = *reinterpret_cast<const f32x4*>(p + dir * (s0 + k) * size);
+    for (int k = 0; k < AT_ONCE; ++k)
+      if (s0 + k < count) {
+        added[k] = *reinterpret_cast<const f32x4*>(p + dir * (s0 + k) * size);
+        fade[k] = static_cast<float>(scalar[dir * (s0 + k)]);
+      }
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < AT_ONCE; ++k) {
       const int s = s0 + k;
       if (s < slots) *reinterpret_cast<f32x4*>(p + dir * s * size) = S;
-      if (s < count) S = S * exp2_raw(static_cast<float>(fades[dir * s])) + added[k];
+      if (s < count) S = S * exp2_raw(fade[k]) + added[k];
     }
   }
   return S;
