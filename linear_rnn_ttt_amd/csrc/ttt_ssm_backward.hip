@@ -29,8 +29,8 @@
 // segments behind the first walk backward for what they add to the adjoint in
 // front of them; (2) the states in front of the segments and the adjoints
 // behind them; (3) the gradients, each segment's tiles last to first with A
-// in registers; (4) the sums of da and dd over batch and segments in order;
-// (5) where heads share b and c, their db and dc added in order.
+// in registers; (4) the sums of da and dd over batch and segments in order and,
+// where heads share b and c, of their db and dc.
 //
 // In (3) a workgroup has eight waves: wave w and w + 4 share features 16 w ..
 // of x (of dX^T and A; each has one half of A's rows) and rows 16 w .. (and
@@ -545,14 +545,15 @@ __global__ __launch_bounds__(GT, NI == 1 && N <= 64 ? 4 : 2) void ttt_ssm_bwd_k(
   }
 }
 
-// da[h], dd[h]: a wave per head over (batch, segment).
-__global__ __launch_bounds__(64) void ttt_ssm_bwd_sum_k(SsmBackwardArgs a) {
+// da[h], dd[h], by a wave: the sums of (batch, segment).
+__device__ __forceinline__ void sum_head(const SsmBackwardArgs& a, int h, int lane) {
   const SsmArgs& f = a.f;
-  const int h = blockIdx.x, lane = threadIdx.x;
   double da = 0.0, dd = 0.0;
-  for (int64_t i = lane; i < static_cast<int64_t>(f.B) * f.segs; i += 64) {
-    const size_t b = i / f.segs, seg = i - b * f.segs;
-    const float* p = a.ws_sums + ((b * f.H + h) * f.segs + seg) * 2;
+  const uint32_t segs = f.segs, count = static_cast<uint32_t>(f.B) * segs;   // workgroups: < 2^32
+  for (uint32_t i = lane; i < count; i += 64) {
+    const uint32_t b = i / segs, seg = i - b * segs;
+    const f32x2 p = *reinterpret_cast<const f32x2*>(
+        a.ws_sums + ((static_cast<size_t>(b) * f.H + h) * segs + seg) * 2);
     da += p[0];
     dd += p[1];
   }
@@ -564,18 +565,35 @@ __global__ __launch_bounds__(64) void ttt_ssm_bwd_sum_k(SsmBackwardArgs a) {
   }
 }
 
-// db, dc of a group: its heads' in order, four values a thread.
+__host__ __device__ inline uint32_t sum_blocks(int H) { return (H + NT / 64 - 1) / (NT / 64); }
+
+__global__ __launch_bounds__(NT) void ttt_ssm_bwd_sum_k(SsmBackwardArgs a) {
+  const int h = blockIdx.x * (NT / 64) + wave_of(threadIdx.x);
+  if (h < a.f.H) sum_head(a, h, threadIdx.x & 63);
+}
+
+// The same by the first workgroups; by the others db, dc of a group: its heads'
+// in order, four values a thread.
 template <bool BF16>
 __global__ __launch_bounds__(NT) void ttt_ssm_bwd_group_k(SsmBackwardArgs a) {
   const SsmArgs& f = a.f;
+  const uint32_t sums = sum_blocks(f.H);
+  if (blockIdx.x < sums) {
+    const int h = blockIdx.x * (NT / 64) + wave_of(threadIdx.x);
+    if (h < f.H) sum_head(a, h, threadIdx.x & 63);
+    return;
+  }
   const int share = f.H / f.G;
   const uint64_t per = static_cast<uint64_t>(f.T) * f.N / 4;   // vectors of one head
   const uint64_t total = per * f.B * f.G;
-  for (uint64_t i = static_cast<uint64_t>(blockIdx.x) * NT + threadIdx.x; i < total;
-       i += static_cast<uint64_t>(gridDim.x) * NT) {
-    const uint64_t group = i / per, in = i - group * per;   // batch and group
-    const uint64_t at = (group * share * per + in) * 4;     // heads of a group are neighbours
+  for (uint64_t i = static_cast<uint64_t>(blockIdx.x - sums) * NT + threadIdx.x; i < total;
+       i += static_cast<uint64_t>(gridDim.x - sums) * NT) {
+    const uint64_t group = total <= 0xffffffffull   // batch and group
+                               ? static_cast<uint32_t>(i) / static_cast<uint32_t>(per)
+                               : i / per;
+    const uint64_t at = (group * share * per + (i - group * per)) * 4;   // a group's heads are neighbours
     f32x4 db = {0.f, 0.f, 0.f, 0.f}, dc = db;
+#pragma unroll 4
     for (int s = 0; s < share; ++s) {
       db += *reinterpret_cast<const f32x4*>(a.ws_db + at + s * per * 4);
       dc += *reinterpret_cast<const f32x4*>(a.ws_dc + at + s * per * 4);
@@ -605,16 +623,15 @@ hipError_t bwd_launch(const SsmBackwardArgs& a, hipStream_t stream) {
   if ((e = hipGetLastError()) != hipSuccess) return e;
   hipLaunchKernelGGL((ttt_ssm_bwd_k<NI, N>), dim3(units * f.segs), dim3(GT), 0, stream, a);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  hipLaunchKernelGGL(ttt_ssm_bwd_sum_k, dim3(f.H), dim3(64), 0, stream, a);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
   if (a.ws_db) {
     const uint64_t total = static_cast<uint64_t>(f.T) * N / 4 * f.B * f.G;
     const uint64_t need = (total + NT - 1) / NT;
-    hipLaunchKernelGGL((ttt_ssm_bwd_group_k<NI == 1>), dim3(need < 8192 ? need : 8192), dim3(NT),
-                       0, stream, a);
-    e = hipGetLastError();
+    hipLaunchKernelGGL((ttt_ssm_bwd_group_k<NI == 1>),
+                       dim3(sum_blocks(f.H) + (need < 8192 ? need : 8192)), dim3(NT), 0, stream, a);
+  } else {
+    hipLaunchKernelGGL(ttt_ssm_bwd_sum_k, dim3(sum_blocks(f.H)), dim3(NT), 0, stream, a);
   }
-  return e;
+  return hipGetLastError();
 }
 
 }  // namespace
