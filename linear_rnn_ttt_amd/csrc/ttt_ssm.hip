@@ -23,7 +23,7 @@
 // the segments (in place), and ttt_ssm_scan_k starts every segment from its
 // own state.  With one segment only the last runs.
 //
-// At bf16, B4 H32 T8192 N64 (8 segments): states 65 us, join 8, scan 113, 181 in
+// At bf16, B4 H32 T8192 N64 (8 segments): states 64 us, join 7, scan 113, 181 in
 // all.  The scan moves 560 MB, 5.0 TB/s, near the 5.4 that a copy reaches on this
 // card; the states, which read x and b once more, 3.9 TB/s (a kernel that only
 // reads reached 4.0).  The scan's vector unit is 54 % busy, its matrix unit 25 %.

@@ -42,8 +42,8 @@
 // so that dX, dB and dC come whole from their products; they are written by
 // rows and read by rows or, transposed, by columns.
 //
-// At bf16, B8 H12 T2048 N64: walks 31 us (4.8 TB/s with the states of every tile
-// that they write), join 7, gradients 90, sums 4.  The gradients are bound
+// At bf16, B8 H12 T2048 N64: walks 32 us (4.7 TB/s with the states of every tile
+// that they write), join 7, gradients 87, sums 4.  The gradients are bound
 // by the vector unit (56 % busy: splitting into parts, decays and the sums over
 // Z) and by waiting between the four barriers of a tile (44 % of the waves' time);
 // the matrix unit is 16 % busy, and the 278 MB that they move would take 52 us.
