@@ -22,8 +22,9 @@ __all__ = ["ttt_rms_norm_forward", "ttt_rms_norm_forward_f8", "ttt_rms_norm_back
 
 F8 = torch.float8_e4m3fn
 
-# the handle of a device's current stream, without a Stream object around it
-# where this torch has that
+# the current device, and the handle of its current stream without a Stream
+# object around it, where this torch has them directly
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                           lambda index: torch.cuda.current_stream(index).cuda_stream)
 
@@ -97,7 +98,7 @@ def _call(func, device, *args):
     """The library's function on the device's current stream; it launches on
     the current device."""
     index = device.index
-    if index == torch.cuda.current_device():
+    if index == _current_device():
         rc = getattr(_lib.lib(), func)(*args, _current_stream(index))
     else:
         with torch.cuda.device(device):
