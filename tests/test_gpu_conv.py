@@ -25,7 +25,10 @@ def make(B, H, T, d, K, dtype, seed=0):
 CASES = [(1, 1, 1, 8, 2, True, True), (2, 3, 2, 64, 4, True, True), (1, 2, 3, 64, 4, True, False),
          (2, 2, 9, 32, 3, False, True), (1, 3, 257, 64, 4, True, True),
          (3, 2, 256, 128, 2, True, False), (1, 2, 33, 24, 3, True, True),
-         (1, 1, 300, 1024, 4, True, True), (2, 1, 65, 200, 4, False, False)]
+         (1, 1, 300, 1024, 4, True, True), (2, 1, 65, 200, 4, False, False),
+         # several of the backward's chunks of 2048, 672 and 64 tokens, the last one ragged
+         (1, 2, 2100, 8, 3, True, True), (2, 1, 1349, 24, 4, True, True),
+         (1, 2, 130, 512, 2, True, True)]
 
 
 @pytest.mark.parametrize("dtype", TYPES, ids=["bf16", "f32"])
